@@ -73,6 +73,7 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1 } pkv_dtype;
 #define PKV_DEVFLAG_BLOCK_RANGE   0x2u  /* decode: table entry outside [0, num_blocks) (block 0 read instead) */
 #define PKV_DEVFLAG_CONTEXT_RANGE 0x4u  /* decode: context_len < 0 or > max_blocks*block_size (clamped) */
 #define PKV_DEVFLAG_WAIT_TIMEOUT  0x8u  /* decode: a shared-memory pipeline wait gave up (output invalid) */
+#define PKV_DEVFLAG_INDEX_RANGE   0x10u /* trees: a parent that is not an earlier node; compact: kept positions that do not ascend */
 
 /* Human-readable name of a status code (static string). */
 const char *pkv_status_str(pkv_status s);
@@ -345,6 +346,147 @@ pkv_status pkv_paged_attention_decode_static_workspace(
     int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
     float scale, int partition_tokens, void *out, pkv_dtype dtype, void *stream);
 
+/* ---- speculative decoding with drafted token trees ----------------------
+ *
+ * A step drafts a tree of tokens for each sequence, computes all of them in
+ * one pass over the cache, and keeps the path that the target model's own
+ * answers confirm:
+ *
+ *   pkv_kv_cache_write         the drafted tokens' K/V, behind the sequence's
+ *                              committed tokens (slot_mapping, [MH] 2.1, 3.3)
+ *   pkv_draft_tree_mask        parents -> ancestor bits and positions, once a step
+ *   pkv_paged_attention_tree   the drafted tokens' attention, once a layer
+ *   pkv_draft_tree_accept      the accepted path, once a step
+ *   pkv_kv_cache_compact       the path's cells moved together, once a step for
+ *                              all layers
+ *   pkv_alloc_truncate         the pages behind the new length released
+ *
+ * The pages describe the cache that this works on; trees are not on them.
+ *
+ * Rows are packed as for pkv_paged_attention_prefill: sequence b's n_b nodes
+ * are rows query_start[b] .. query_start[b+1]-1 (ascending starts, n_b <=
+ * max_query_len <= PKV_TREE_MAX_NODES, n_b = 0 allowed), and they are the last
+ * n_b of its context_lens[b] tokens: node i is cell context_lens[b] - n_b + i.
+ * A sequence whose rows or lengths contradict these bounds sets
+ * PKV_DEVFLAG_CONTEXT_RANGE and is skipped.  Rows outside every sequence are
+ * left as they were.
+ */
+#define PKV_TREE_MAX_NODES 1024
+
+/*
+ * draft_tree_mask -- ancestor bits and positions of drafted nodes.
+ *
+ *   parents        [num_tokens] int32: a node's parent as an index within its
+ *                  sequence's nodes, below the node's own, or -1 (a root)  read
+ *   query_start    [batch + 1], context_lens [batch] int32                 read
+ *   tree_mask      [num_tokens, words] int32, words = ceil(max_query_len / 32):
+ *                  bit j % 32 of word j / 32 of node i's row is 1 when node j
+ *                  is i or one of i's ancestors                         written
+ *   positions      [num_tokens] int32: context_lens[b] - n_b + depth, the
+ *                  position that the node's token would have (a root has depth
+ *                  0)                                                   written
+ *
+ * Any other parent sets PKV_DEVFLAG_INDEX_RANGE; that node becomes a root.
+ */
+pkv_status pkv_draft_tree_mask(const int32_t *parents, int num_tokens, const int32_t *query_start,
+                               int max_query_len, const int32_t *context_lens, int batch,
+                               int32_t *tree_mask, int32_t *positions, void *stream);
+
+/*
+ * paged_attention_tree -- each drafted node attends over its sequence's
+ * committed tokens and over the nodes that its mask row names.
+ *
+ *   query          [num_tokens, num_heads, head_dim]                  device, read
+ *   tree_mask      [num_tokens, ceil(max_query_len / 32)] int32 as above; any
+ *                  bits will do (bits of nodes past n_b are ignored)  device, read
+ *   caches, block_tables, context_lens   as for pkv_paged_attention_decode
+ *   workspace      pkv_tree_workspace_bytes(...) bytes                device, scratch
+ *   out            [num_tokens, num_heads, head_dim]                  device, written
+ *
+ * For node i of sequence b (query head h, kv head h / group):
+ *   out = sum_j softmax_j(scale <q, K_j>) V_j   over the cells j of b with
+ *   j < context_lens[b] - n_b, or bit j - (context_lens[b] - n_b) of i's row
+ * with the softmax over exactly these cells; none of them gives a zero row.
+ * Cells past context_lens[b] are never read.  Shapes as for the other calls
+ * (group size 1..8, head_dim 64 / 128, block_size 16 / 32); max_query_len <=
+ * PKV_TREE_MAX_NODES, else PKV_ERR_UNSUPPORTED.
+ */
+size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_heads, int num_kv_heads,
+                                int head_dim, int max_blocks, int block_size);
+pkv_status pkv_paged_attention_tree(const void *query, int num_tokens, const int32_t *query_start,
+                                    int max_query_len, const int32_t *tree_mask,
+                                    const void *key_cache, const void *value_cache,
+                                    const int32_t *block_tables, int max_blocks,
+                                    const int32_t *context_lens, int batch, int num_heads,
+                                    int num_kv_heads, int head_dim, int block_size,
+                                    int64_t num_blocks, float scale, void *workspace,
+                                    size_t workspace_bytes, void *out, pkv_dtype dtype,
+                                    void *stream);
+
+/*
+ * draft_tree_accept -- greedy verification: from node 0 on, the next accepted
+ * node is the lowest child of the accepted one whose drafted token is the
+ * target model's answer there.
+ *
+ *   draft_tokens   [num_tokens] int64: the node's token                    read
+ *   target_tokens  [num_tokens] int64: the target's token after the node   read
+ *   parents, query_start   as above                                        read
+ *   accept_path    [batch, max_query_len] int32: the accepted nodes in order
+ *                  (they ascend), then -1                               written
+ *   accept_lens    [batch] int32: their number (0 for n_b = 0)          written
+ *   next_tokens    [batch] int64: the target's token after the last
+ *                  accepted node, -1 for n_b = 0                        written
+ *
+ * Node 0 is the sequence's own last token and always accepted; other roots
+ * never are.  A parent that is not an earlier node sets
+ * PKV_DEVFLAG_INDEX_RANGE and its node is never accepted.  A skipped sequence
+ * gets an empty path.
+ */
+pkv_status pkv_draft_tree_accept(const int64_t *draft_tokens, const int64_t *target_tokens,
+                                 const int32_t *parents, int num_tokens, const int32_t *query_start,
+                                 int max_query_len, int batch, int32_t *accept_path,
+                                 int32_t *accept_lens, int64_t *next_tokens, void *stream);
+
+/*
+ * kv_cache_compact -- move the kept cells of each sequence together, in place,
+ * in the caches of every layer: cell start_lens[b] + keep[b][i] goes to cell
+ * start_lens[b] + i, K and V, for 0 <= i < keep_lens[b].
+ *
+ *   key_caches,
+ *   value_caches   host arrays of num_layers device pointers, each
+ *                  [num_blocks, block_size, num_kv_heads, head_dim], all
+ *                  different                              read and written
+ *   block_tables   [batch, max_blocks] int32              device, read
+ *   start_lens     [batch] int32: the cell that the first kept one moves to
+ *                                                         device, read
+ *   keep           [batch, max_keep] int32: ascending positions behind
+ *                  start_lens[b]; entries from keep_lens[b] on are not read
+ *                                                         device, read
+ *   keep_lens      [batch] int32, 0 .. max_keep           device, read
+ *   workspace      pkv_compact_workspace_bytes(...) bytes device, scratch
+ *
+ * With start_lens = the lengths before drafting, keep = accept_path and
+ * keep_lens = accept_lens this is the last step of a tree verification; with a
+ * list of positions from all over a context it drops the others from the
+ * cache.  The result is as if all cells were read before any is written.
+ * Cells from start_lens[b] + keep_lens[b] on keep what they held.  The pages
+ * that are written must belong to one sequence of the call alone (copy shared
+ * pages first).  A negative start, a count outside 0 .. max_keep or a range
+ * past the table sets PKV_DEVFLAG_CONTEXT_RANGE and the sequence is skipped;
+ * kept positions that do not ascend or lie past the table set
+ * PKV_DEVFLAG_INDEX_RANGE and a page id outside the pool
+ * PKV_DEVFLAG_BLOCK_RANGE: such moves are left out, and what the sequence's
+ * cells from start_lens[b] on then hold is not specified.
+ */
+size_t pkv_compact_workspace_bytes(int num_layers, int batch, int max_keep, int num_kv_heads,
+                                   int head_dim);
+pkv_status pkv_kv_cache_compact(void *const *key_caches, void *const *value_caches, int num_layers,
+                                const int32_t *block_tables, int max_blocks,
+                                const int32_t *start_lens, const int32_t *keep, int max_keep,
+                                const int32_t *keep_lens, int batch, int num_kv_heads, int head_dim,
+                                int64_t num_blocks, int block_size, void *workspace,
+                                size_t workspace_bytes, pkv_dtype dtype, void *stream);
+
 /* ---- host block allocator ([YK] 二; [FC] 二.2 steps 1, 2, 4 and 二.3) ------
  *
  * A pool of num_blocks physical block ids with a free list and per-block
@@ -393,6 +535,14 @@ pkv_status pkv_alloc_append(pkv_alloc *a, int32_t *blocks, int capacity, int *n,
  * to the free list.  PKV_ERR_OUT_OF_RANGE (nothing changed) if an id is
  * outside the pool or already free. */
 pkv_status pkv_alloc_free(pkv_alloc *a, const int32_t *blocks, int n);
+
+/*
+ * Shrink a sequence to new_len tokens: the blocks of its table behind
+ * ceil(new_len / block_size) are released as by pkv_alloc_free and *n becomes
+ * that number.  A table that is already as short is left as it is; new_len < 0
+ * is PKV_ERR_INVALID_ARG.  On an error nothing changes.
+ */
+pkv_status pkv_alloc_truncate(pkv_alloc *a, const int32_t *blocks, int *n, int64_t new_len);
 
 /* ---- automatic prefix caching ([FC] 五.4; [MH] 2.3) --------------------
  *

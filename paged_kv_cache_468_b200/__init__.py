@@ -11,18 +11,24 @@ from .pagedkv import (  # noqa: F401
     F16,
     BlockAllocator,
     PagedKVError,
+    compact_workspace_bytes,
     copy_blocks,
     decode_cascade_plan,
     decode_plan,
     decode_workspace_bytes,
     device_flags,
+    draft_tree_accept,
+    draft_tree_mask,
     hbm_gather_probe,
     hbm_read_probe,
+    kv_cache_compact,
     kv_cache_write,
     lib,
     paged_attention_decode,
     paged_attention_decode_cascade,
     paged_attention_prefill,
+    paged_attention_tree,
     selftest_bounded_wait,
+    tree_workspace_bytes,
     version,
 )

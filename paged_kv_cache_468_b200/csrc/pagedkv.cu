@@ -18,6 +18,8 @@
 #include "pagedkv.h"
 #include "pkv_kernels.cuh"
 #include "pkv_prefill.cuh"
+#include "pkv_tree.cuh"
+#include "pkv_compact.cuh"
 
 namespace {
 
@@ -1123,4 +1125,239 @@ extern "C" pkv_status pkv_paged_attention_decode_static_workspace(
                                       context_lens, batch, num_heads, num_kv_heads, head_dim,
                                       block_size, num_blocks, scale, partition_tokens, ws,
                                       need > 0 ? kStaticWorkspaceBytes : 0, out, dtype, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Speculative decoding: drafted token trees
+// ---------------------------------------------------------------------------
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// What the tree calls share: row counts and the size of a tree.
+pkv_status check_tree(int num_tokens, int max_query_len, int batch)
+{
+    if (num_tokens < 0 || max_query_len < 0 || batch < 0)
+        return fail(PKV_ERR_INVALID_ARG, "num_tokens=%d max_query_len=%d batch=%d", num_tokens,
+                    max_query_len, batch);
+    if (max_query_len > PKV_TREE_MAX_NODES)
+        return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d (at most %d nodes per tree)", max_query_len,
+                    PKV_TREE_MAX_NODES);
+    if (batch > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "batch %d (at most 65535)", batch);
+    return PKV_OK;
+}
+
+static_assert(pkv::kTreeMaxNodes == PKV_TREE_MAX_NODES, "tree size");
+
+}  // namespace
+
+extern "C" pkv_status pkv_draft_tree_mask(const int32_t *parents, int num_tokens,
+                                          const int32_t *query_start, int max_query_len,
+                                          const int32_t *context_lens, int batch, int32_t *tree_mask,
+                                          int32_t *positions, void *stream)
+{
+    pkv_status s = check_tree(num_tokens, max_query_len, batch);
+    if (s != PKV_OK)
+        return s;
+    if (batch == 0 || num_tokens == 0 || max_query_len == 0)
+        return PKV_OK;
+    if (!parents || !query_start || !context_lens || !tree_mask || !positions)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned4(parents) || !aligned4(query_start) || !aligned4(context_lens) || !aligned4(tree_mask) ||
+        !aligned4(positions))
+        return fail(PKV_ERR_MISALIGNED, "parents/query_start/context_lens/tree_mask/positions must be 4-byte aligned");
+    const int words = (max_query_len + 31) / 32;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto kern, int nw) {
+        const dim3 grid((unsigned)((words + nw - 1) / nw), (unsigned)batch);
+        return launch_pdl(kern, grid, dim3((unsigned)nw * 32), 0, st, parents, num_tokens, query_start,
+                          max_query_len, context_lens, words, tree_mask, positions);
+    };
+    const cudaError_t e = words <= 2 ? go(pkv::tree_mask_kernel<2>, 2) : go(pkv::tree_mask_kernel<8>, 8);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_mask_kernel launch");
+    return PKV_OK;
+}
+
+extern "C" pkv_status pkv_draft_tree_accept(const int64_t *draft_tokens, const int64_t *target_tokens,
+                                            const int32_t *parents, int num_tokens,
+                                            const int32_t *query_start, int max_query_len, int batch,
+                                            int32_t *accept_path, int32_t *accept_lens,
+                                            int64_t *next_tokens, void *stream)
+{
+    pkv_status s = check_tree(num_tokens, max_query_len, batch);
+    if (s != PKV_OK)
+        return s;
+    if (batch == 0)
+        return PKV_OK;
+    if (!query_start || !accept_lens || !next_tokens || (max_query_len > 0 && !accept_path) ||
+        (num_tokens > 0 && (!draft_tokens || !target_tokens || !parents)))
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned8(draft_tokens) || !aligned8(target_tokens) || !aligned8(next_tokens))
+        return fail(PKV_ERR_MISALIGNED, "draft_tokens/target_tokens/next_tokens must be 8-byte aligned");
+    if (!aligned4(parents) || !aligned4(query_start) || !aligned4(accept_path) || !aligned4(accept_lens))
+        return fail(PKV_ERR_MISALIGNED, "parents/query_start/accept_path/accept_lens must be 4-byte aligned");
+    const cudaError_t e = launch_pdl(pkv::tree_accept_kernel, dim3((unsigned)batch), dim3(pkv::kAcceptThreads), 0,
+                                     static_cast<cudaStream_t>(stream), draft_tokens, target_tokens, parents,
+                                     num_tokens, query_start, max_query_len, accept_path, accept_lens,
+                                     next_tokens);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_accept_kernel launch");
+    return PKV_OK;
+}
+
+extern "C" size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_heads, int num_kv_heads,
+                                           int head_dim, int max_blocks, int block_size)
+{
+    if (check_shapes(batch, num_heads, num_kv_heads, head_dim, max_blocks, block_size) != PKV_OK ||
+        check_tree(0, max_query_len, batch) != PKV_OK)
+        return 0;
+    return 0;
+}
+
+extern "C" pkv_status pkv_paged_attention_tree(
+    const void *query, int num_tokens, const int32_t *query_start, int max_query_len,
+    const int32_t *tree_mask, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks, const int32_t *context_lens, int batch, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale, void *workspace,
+    size_t workspace_bytes, void *out, pkv_dtype dtype, void *stream)
+{
+    pkv_status s = check_shapes(batch, num_heads, num_kv_heads, head_dim, max_blocks, block_size);
+    if (s == PKV_OK)
+        s = check_tree(num_tokens, max_query_len, batch);
+    if (s != PKV_OK)
+        return s;
+    if (dtype != PKV_F16 && dtype != PKV_BF16)
+        return fail(PKV_ERR_INVALID_ARG, "dtype %d", (int)dtype);
+    if (num_blocks <= 0 || num_blocks * block_size >= ((int64_t)1 << 31))
+        return fail(PKV_ERR_INVALID_ARG, "num_blocks %lld: need 0 < num_blocks*block_size < 2^31",
+                    (long long)num_blocks);
+    if (!std::isfinite(scale))
+        return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+    if (batch == 0 || max_query_len == 0 || num_tokens == 0)
+        return PKV_OK;
+    if (!query || !query_start || !tree_mask || !key_cache || !value_cache || !block_tables ||
+        !context_lens || !out)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(out))
+        return fail(PKV_ERR_MISALIGNED, "query/cache/out pointers must be 16-byte aligned");
+    if (!aligned4(query_start) || !aligned4(tree_mask) || !aligned4(block_tables) || !aligned4(context_lens))
+        return fail(PKV_ERR_MISALIGNED, "query_start/tree_mask/block_tables/context_lens must be 4-byte aligned");
+    const size_t need = pkv_tree_workspace_bytes(batch, max_query_len, num_heads, num_kv_heads, head_dim,
+                                                 max_blocks, block_size);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                        workspace ? workspace_bytes : (size_t)0);
+        if (!aligned16(workspace))
+            return fail(PKV_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    }
+    pkv::TreeArgs a;
+    a.query = static_cast<const uint16_t *>(query);
+    a.query_start = query_start;
+    a.tree_mask = tree_mask;
+    a.key_cache = static_cast<const uint16_t *>(key_cache);
+    a.value_cache = static_cast<const uint16_t *>(value_cache);
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.out = static_cast<uint16_t *>(out);
+    a.batch = batch;
+    a.num_tokens = num_tokens;
+    a.max_query_len = max_query_len;
+    a.words = (max_query_len + 31) / 32;
+    a.max_blocks = max_blocks;
+    a.block_size = block_size;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = num_heads / num_kv_heads;
+    a.num_blocks = (int)num_blocks;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, dim3((unsigned)num_tokens, (unsigned)num_kv_heads), dim3(128), 0,
+                          static_cast<cudaStream_t>(stream), a);
+    };
+    const cudaError_t e =
+        head_dim == 64 ? (dtype == PKV_BF16 ? go(pkv::tree_attend_kernel<64, true>) : go(pkv::tree_attend_kernel<64, false>))
+                       : (dtype == PKV_BF16 ? go(pkv::tree_attend_kernel<128, true>) : go(pkv::tree_attend_kernel<128, false>));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_attend_kernel launch");
+    return PKV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Compaction of kept cells
+// ---------------------------------------------------------------------------
+extern "C" size_t pkv_compact_workspace_bytes(int num_layers, int batch, int max_keep, int num_kv_heads,
+                                              int head_dim)
+{
+    (void)num_layers, (void)batch, (void)max_keep, (void)num_kv_heads, (void)head_dim;
+    return 0;
+}
+
+extern "C" pkv_status pkv_kv_cache_compact(void *const *key_caches, void *const *value_caches,
+                                           int num_layers, const int32_t *block_tables, int max_blocks,
+                                           const int32_t *start_lens, const int32_t *keep, int max_keep,
+                                           const int32_t *keep_lens, int batch, int num_kv_heads,
+                                           int head_dim, int64_t num_blocks, int block_size,
+                                           void *workspace, size_t workspace_bytes, pkv_dtype dtype,
+                                           void *stream)
+{
+    if (num_layers < 0 || max_blocks <= 0 || max_keep < 0 || batch < 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        block_size <= 0)
+        return fail(PKV_ERR_INVALID_ARG, "num_layers=%d max_blocks=%d max_keep=%d batch=%d num_kv_heads=%d "
+                    "head_dim=%d block_size=%d", num_layers, max_blocks, max_keep, batch, num_kv_heads,
+                    head_dim, block_size);
+    if (dtype != PKV_F16 && dtype != PKV_BF16)
+        return fail(PKV_ERR_INVALID_ARG, "dtype %d", (int)dtype);
+    if (num_blocks <= 0 || num_blocks > INT32_MAX || num_blocks * block_size >= ((int64_t)1 << 31))
+        return fail(PKV_ERR_INVALID_ARG, "num_blocks %lld: need 0 < num_blocks*block_size < 2^31",
+                    (long long)num_blocks);
+    if ((int64_t)max_blocks * block_size >= (int64_t)1 << 30)
+        return fail(PKV_ERR_INVALID_ARG, "max_blocks * block_size too large");
+    if (head_dim % 8 != 0)
+        return fail(PKV_ERR_UNSUPPORTED, "head_dim %d: rows must be a multiple of 16 bytes", head_dim);
+    if ((int64_t)num_kv_heads * head_dim > (int64_t)1 << 24)
+        return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads * head_dim too large");
+    if (batch > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "batch %d (at most 65535)", batch);
+    if (num_layers == 0 || batch == 0 || max_keep == 0)
+        return PKV_OK;
+    if (!key_caches || !value_caches || !block_tables || !start_lens || !keep || !keep_lens)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned4(block_tables) || !aligned4(start_lens) || !aligned4(keep) || !aligned4(keep_lens))
+        return fail(PKV_ERR_MISALIGNED, "block_tables/start_lens/keep/keep_lens must be 4-byte aligned");
+    for (int i = 0; i < num_layers; ++i) {
+        if (!key_caches[i] || !value_caches[i])
+            return fail(PKV_ERR_INVALID_ARG, "null cache pointer (layer %d)", i);
+        if (!aligned16(key_caches[i]) || !aligned16(value_caches[i]))
+            return fail(PKV_ERR_MISALIGNED, "cache pointers must be 16-byte aligned (layer %d)", i);
+    }
+    pkv::CompactArgs a;
+    a.block_tables = block_tables;
+    a.start_lens = start_lens;
+    a.keep = keep;
+    a.keep_lens = keep_lens;
+    a.max_blocks = max_blocks;
+    a.max_keep = max_keep;
+    a.block_size = block_size;
+    a.num_blocks = (int)num_blocks;
+    a.vec_per_cell = num_kv_heads * head_dim / 8;
+    for (int l0 = 0; l0 < num_layers; l0 += pkv::kCompactMaxLayers) {
+        const int layers = std::min(num_layers - l0, pkv::kCompactMaxLayers);
+        for (int i = 0; i < 2 * pkv::kCompactMaxLayers; ++i)
+            a.cache[i] = nullptr;
+        for (int i = 0; i < layers; ++i) {
+            a.cache[i] = static_cast<uint4 *>(key_caches[l0 + i]);
+            a.cache[layers + i] = static_cast<uint4 *>(value_caches[l0 + i]);
+        }
+        const dim3 grid((unsigned)((a.vec_per_cell + pkv::kCompactThreads - 1) / pkv::kCompactThreads),
+                        (unsigned)(2 * layers), (unsigned)batch);
+        const cudaError_t e = launch_pdl(pkv::compact_kernel, grid, dim3(pkv::kCompactThreads), 0,
+                                         static_cast<cudaStream_t>(stream), a);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "compact_kernel launch");
+    }
+    return PKV_OK;
 }

@@ -246,6 +246,22 @@ pkv_status pkv_alloc_free(pkv_alloc *a, const int32_t *blocks, int n)
     return PKV_OK;
 }
 
+pkv_status pkv_alloc_truncate(pkv_alloc *a, const int32_t *blocks, int *n, int64_t new_len)
+{
+    if (!a || !n || *n < 0 || new_len < 0)
+        return err(PKV_ERR_INVALID_ARG, "truncate: bad handle, count or length");
+    const int64_t bs = a->block_size;
+    const int64_t keep = new_len / bs + (new_len % bs != 0);
+    if (keep >= *n)
+        return PKV_OK;
+    if (!blocks)
+        return err(PKV_ERR_INVALID_ARG, "truncate: no block list");
+    const pkv_status s = pkv_alloc_free(a, blocks + keep, *n - (int)keep);
+    if (s == PKV_OK)
+        *n = (int)keep;
+    return s;
+}
+
 // ---- automatic prefix caching -------------------------------------------
 // A full block is named by a hash of its tokens chained with the previous
 // block's hash, so equal hashes mean equal token prefixes up to the block's

@@ -21,6 +21,8 @@ LIB_PATH = os.environ.get("PKV_LIBRARY") or os.path.join(_HERE, "libpagedkv.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OUT_OF_RANGE, ERR_OOM, ERR_CUDA, ERR_WORKSPACE, \
     ERR_MISALIGNED = range(8)
 DEVFLAG_SLOT_RANGE, DEVFLAG_BLOCK_RANGE, DEVFLAG_CONTEXT_RANGE, DEVFLAG_WAIT_TIMEOUT = 1, 2, 4, 8
+DEVFLAG_INDEX_RANGE = 16
+TREE_MAX_NODES = 1024
 F16, BF16 = 0, 1
 _DTYPES = {torch.float16: F16, torch.bfloat16: BF16}
 
@@ -107,6 +109,22 @@ def lib() -> ctypes.CDLL:
         L.pkv_alloc_new_seq_cached.restype = i32
         L.pkv_alloc_new_seq_cached.argtypes = [P, ctypes.POINTER(ctypes.c_uint64), i32, i64, pi32,
                                                i32, pint, pint]
+        L.pkv_alloc_truncate.restype = i32
+        L.pkv_alloc_truncate.argtypes = [P, pi32, pint, i64]
+        L.pkv_draft_tree_mask.restype = i32
+        L.pkv_draft_tree_mask.argtypes = [P, i32, P, i32, P, i32, P, P, P]
+        L.pkv_draft_tree_accept.restype = i32
+        L.pkv_draft_tree_accept.argtypes = [P, P, P, i32, P, i32, i32, P, P, P, P]
+        L.pkv_tree_workspace_bytes.restype = sz
+        L.pkv_tree_workspace_bytes.argtypes = [i32] * 7
+        L.pkv_paged_attention_tree.restype = i32
+        L.pkv_paged_attention_tree.argtypes = [P, i32, P, i32, P, P, P, P, i32, P, i32, i32, i32, i32,
+                                               i32, i64, f32, P, sz, P, i32, P]
+        L.pkv_compact_workspace_bytes.restype = sz
+        L.pkv_compact_workspace_bytes.argtypes = [i32] * 5
+        L.pkv_kv_cache_compact.restype = i32
+        L.pkv_kv_cache_compact.argtypes = [P, P, i32, P, i32, P, P, i32, P, i32, i32, i32, i64, i32, P,
+                                           sz, i32, P]
         L.pkv_hbm_read_probe.restype = i32
         L.pkv_hbm_read_probe.argtypes = [P, sz, P, i32, P]
         L.pkv_hbm_gather_probe.restype = i32
@@ -385,6 +403,181 @@ def paged_attention_decode_cascade(query: torch.Tensor, key_cache: torch.Tensor,
     return out
 
 
+# ---- speculative decoding with drafted token trees ----
+def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
+    """Address of a dense CUDA tensor of this type and shape on `device`."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')} {list(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return _dev(t, name)
+
+
+def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new tensor whose memory the caching allocator reuses in `stream`'s order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, device, stream) -> tuple:
+    """(address, bytes, tensor to keep alive) of a workspace of `need` bytes."""
+    if not need:
+        return None, 0, None
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, device, stream)
+    elif workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+
+
+def _on_device(device: torch.device):
+    """The device made current for a launch (the stream belongs to it)."""
+    return torch.cuda.device(device)
+
+
+def _tree_rows(query_start: torch.Tensor, max_query_len: int) -> int:
+    if query_start.dim() != 1 or query_start.shape[0] < 1:
+        raise ValueError("query_start must be int32 [batch + 1]")
+    if not 0 <= int(max_query_len) <= TREE_MAX_NODES:
+        raise ValueError(f"max_query_len must be 0 .. {TREE_MAX_NODES}")
+    return query_start.shape[0] - 1
+
+
+def draft_tree_mask(parents: torch.Tensor, query_start: torch.Tensor, max_query_len: int,
+                    context_lens: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> tuple:
+    """Ancestor bits and positions of drafted nodes (see include/pagedkv.h).
+    parents int32 [T] (index within the sequence's nodes, -1 for a root), query_start int32 [B+1],
+    context_lens int32 [B] (the drafted tokens included) -> tree_mask int32 [T, ceil(max_query_len / 32)],
+    positions int32 [T].  Rows of T outside every sequence are not written."""
+    B = _tree_rows(query_start, max_query_len)
+    dev = parents.device
+    T, W = parents.shape[0] if parents.dim() == 1 else -1, -(-int(max_query_len) // 32)
+    args = (_tensor(parents, "parents", torch.int32, (T,), dev), T,
+            _tensor(query_start, "query_start", torch.int32, (B + 1,), dev), int(max_query_len),
+            _tensor(context_lens, "context_lens", torch.int32, (B,), dev), B)
+    mask = _empty((T, W), torch.int32, dev, stream)
+    positions = _empty((T,), torch.int32, dev, stream)
+    with _on_device(dev):
+        st = lib().pkv_draft_tree_mask(*args, _dev(mask, "tree_mask"), _dev(positions, "positions"),
+                                       _stream_handle(stream, dev))
+    _check(st, "pkv_draft_tree_mask")
+    return mask, positions
+
+
+def draft_tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, parents: torch.Tensor,
+                      query_start: torch.Tensor, max_query_len: int,
+                      stream: Optional[torch.cuda.Stream] = None) -> tuple:
+    """Greedy verification of drafted trees (see include/pagedkv.h).  draft_tokens / target_tokens
+    int64 [T], parents int32 [T], query_start int32 [B+1] -> accept_path int32 [B, max_query_len]
+    (accepted nodes, then -1), accept_lens int32 [B], next_tokens int64 [B]."""
+    B = _tree_rows(query_start, max_query_len)
+    dev = parents.device
+    T = parents.shape[0] if parents.dim() == 1 else -1
+    args = (_tensor(draft_tokens, "draft_tokens", torch.int64, (T,), dev),
+            _tensor(target_tokens, "target_tokens", torch.int64, (T,), dev),
+            _tensor(parents, "parents", torch.int32, (T,), dev), T,
+            _tensor(query_start, "query_start", torch.int32, (B + 1,), dev), int(max_query_len), B)
+    path = _empty((B, int(max_query_len)), torch.int32, dev, stream)
+    lens = _empty((B,), torch.int32, dev, stream)
+    following = _empty((B,), torch.int64, dev, stream)
+    with _on_device(dev):
+        st = lib().pkv_draft_tree_accept(*args, _dev(path, "accept_path"), _dev(lens, "accept_lens"),
+                                         _dev(following, "next_tokens"), _stream_handle(stream, dev))
+    _check(st, "pkv_draft_tree_accept")
+    return path, lens, following
+
+
+def tree_workspace_bytes(batch: int, max_query_len: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                         max_blocks: int, block_size: int) -> int:
+    return int(lib().pkv_tree_workspace_bytes(batch, max_query_len, num_heads, num_kv_heads, head_dim,
+                                              max_blocks, block_size))
+
+
+def paged_attention_tree(query: torch.Tensor, query_start: torch.Tensor, max_query_len: int,
+                         tree_mask: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of drafted token trees over the paged cache (see include/pagedkv.h).
+    query [T, Hq, D], query_start int32 [B+1], tree_mask int32 [T, ceil(max_query_len / 32)] (bit j of
+    a row: node j is seen), caches [NB, bs, Hkv, D], block_tables int32 [B, max_blocks], context_lens
+    int32 [B] (the drafted tokens included) -> out [T, Hq, D].  A workspace tensor (at least
+    tree_workspace_bytes(...) bytes) is allocated by torch when not given."""
+    if query.dim() != 3:
+        raise ValueError("query must be [total_tokens, num_heads, head_dim]")
+    if key_cache.dim() != 4 or key_cache.shape != value_cache.shape:
+        raise ValueError("caches must both be [num_blocks, block_size, num_kv_heads, head_dim]")
+    B = _tree_rows(query_start, max_query_len)
+    dev, dt = query.device, _dtype_code(query)
+    T, Hq, D = query.shape
+    NB, bs, Hkv, D2 = key_cache.shape
+    if D2 != D:
+        raise ValueError("head_dim differs between query and caches")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be int32 [batch, max_blocks]")
+    MB, W = block_tables.shape[1], -(-int(max_query_len) // 32)
+    head = (_tensor(query, "query", query.dtype, (T, Hq, D), dev), T,
+            _tensor(query_start, "query_start", torch.int32, (B + 1,), dev), int(max_query_len),
+            _tensor(tree_mask, "tree_mask", torch.int32, (T, W), dev),
+            _tensor(key_cache, "key_cache", query.dtype, (NB, bs, Hkv, D), dev),
+            _tensor(value_cache, "value_cache", query.dtype, (NB, bs, Hkv, D), dev),
+            _tensor(block_tables, "block_tables", torch.int32, (B, MB), dev), MB,
+            _tensor(context_lens, "context_lens", torch.int32, (B,), dev), B, Hq, Hkv, D, bs, NB,
+            float(scale))
+    if out is None:
+        out = _empty((T, Hq, D), query.dtype, dev, stream)
+    out_ptr = _tensor(out, "out", query.dtype, (T, Hq, D), dev)
+    ws_ptr, ws_bytes, workspace = _scratch(
+        workspace, tree_workspace_bytes(B, int(max_query_len), Hq, Hkv, D, MB, bs), dev, stream)
+    with _on_device(dev):
+        st = lib().pkv_paged_attention_tree(*head, ws_ptr, ws_bytes, out_ptr, dt, _stream_handle(stream, dev))
+    _check(st, "pkv_paged_attention_tree")
+    return out
+
+
+def compact_workspace_bytes(num_layers: int, batch: int, max_keep: int, num_kv_heads: int,
+                            head_dim: int) -> int:
+    return int(lib().pkv_compact_workspace_bytes(num_layers, batch, max_keep, num_kv_heads, head_dim))
+
+
+def kv_cache_compact(key_caches, value_caches, block_tables: torch.Tensor, start_lens: torch.Tensor,
+                     keep: torch.Tensor, keep_lens: torch.Tensor,
+                     workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Move kept cells together in place (see include/pagedkv.h): cell start_lens[b] + keep[b, i] goes to
+    cell start_lens[b] + i for i < keep_lens[b], in every layer.  key_caches / value_caches: the layers'
+    caches [NB, bs, Hkv, D] (a list, or one tensor for one layer), block_tables int32 [B, max_blocks],
+    start_lens and keep_lens int32 [B], keep int32 [B, max_keep] ascending."""
+    if isinstance(key_caches, torch.Tensor):
+        key_caches, value_caches = [key_caches], [value_caches]
+    if len(key_caches) != len(value_caches) or not len(key_caches):
+        raise ValueError("key_caches and value_caches must list the same layers, at least one")
+    first = key_caches[0]
+    if first.dim() != 4:
+        raise ValueError("caches must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    dev, dt, N = first.device, _dtype_code(first), len(key_caches)
+    NB, bs, Hkv, D = first.shape
+    if block_tables.dim() != 2 or keep.dim() != 2:
+        raise ValueError("block_tables must be int32 [batch, max_blocks], keep int32 [batch, max_keep]")
+    (B, MB), K = block_tables.shape, keep.shape[1]
+    ptrs = [[_tensor(c, name, first.dtype, (NB, bs, Hkv, D), dev) for c in caches]
+            for name, caches in (("key_caches", key_caches), ("value_caches", value_caches))]
+    if len(set(ptrs[0] + ptrs[1])) != 2 * N:
+        raise ValueError("the caches of a call must all be different tensors")
+    args = (_tensor(block_tables, "block_tables", torch.int32, (B, MB), dev), MB,
+            _tensor(start_lens, "start_lens", torch.int32, (B,), dev),
+            _tensor(keep, "keep", torch.int32, (B, K), dev), K,
+            _tensor(keep_lens, "keep_lens", torch.int32, (B,), dev), B, Hkv, D, NB, bs)
+    ws_ptr, ws_bytes, workspace = _scratch(workspace, compact_workspace_bytes(N, B, K, Hkv, D), dev, stream)
+    arr = ctypes.c_void_p * N
+    with _on_device(dev):
+        st = lib().pkv_kv_cache_compact(arr(*ptrs[0]), arr(*ptrs[1]), N, *args, ws_ptr, ws_bytes, dt,
+                                        _stream_handle(stream, dev))
+    _check(st, "pkv_kv_cache_compact")
+
+
 class BlockAllocator:
     """Host block pool with free list, refcounts and copy-on-write (C++ in the library)."""
 
@@ -448,6 +641,13 @@ class BlockAllocator:
 
     def free(self, blocks: list) -> None:
         _check(lib().pkv_alloc_free(self._h, self._arr(blocks), len(blocks)), "pkv_alloc_free")
+
+    def truncate(self, blocks: list, new_len: int) -> None:
+        """Shrink a sequence's table in place to the blocks of new_len tokens; the rest is released."""
+        n = ctypes.c_int(len(blocks))
+        _check(lib().pkv_alloc_truncate(self._h, self._arr(blocks), ctypes.byref(n), int(new_len)),
+               "pkv_alloc_truncate")
+        del blocks[n.value:]
 
     # ---- automatic prefix caching ----
     def block_hashes(self, tokens: list) -> list:
