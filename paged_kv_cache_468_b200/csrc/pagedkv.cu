@@ -1208,13 +1208,82 @@ extern "C" pkv_status pkv_draft_tree_accept(const int64_t *draft_tokens, const i
     return PKV_OK;
 }
 
+namespace {
+
+// CTAs of a tree attention call and the layout of its records.
+struct TreePlan {
+    int ctas, shares;
+    size_t ml, o, total;        // workspace offsets; the descriptors come first
+};
+TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+                   int max_blocks, int block_size)
+{
+    TreePlan p;
+    const int per_tile = pkv::kTreeRows / (num_heads / num_kv_heads);
+    const int row_tiles = (max_query_len + per_tile - 1) / per_tile;
+    p.shares = row_tiles > 1 ? 2 : 1;
+    // two CTAs per SM, fewer where the largest such call has less to share out
+    const int64_t tiles = ((int64_t)max_blocks * block_size + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
+    const int64_t units = (int64_t)batch * num_kv_heads * std::max(1, row_tiles) * (tiles + pkv::kTreeItemCost);
+    p.ctas = (int)std::min<int64_t>(2 * kPlanSmCount, std::max<int64_t>(p.shares, units / pkv::kTreeMinUnits));
+    p.ctas += p.ctas % p.shares;                // pairs
+    const size_t rows = (size_t)p.ctas * 2 * 2 * pkv::kTreeRows;
+    p.ml = align256((size_t)p.ctas * 2 * sizeof(int4));
+    p.o = align256(p.ml + rows * sizeof(float2));
+    p.total = align256(p.o + rows * (size_t)head_dim * sizeof(float));
+    return p;
+}
+
+template <int D, int BS, bool BF16>
+cudaError_t launch_tree(const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a, int ctas,
+                        cudaStream_t st)
+{
+    constexpr int smem = pkv::TreeShape<D>::kSmemBytes;
+    auto kern = pkv::tree_attend_kernel<D, BS, BF16>;
+    static bool configured[64] = {};
+    static std::mutex mu;
+    const int dev = current_device();
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev < 0 || dev >= 64 || !configured[dev]) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess)   // two CTAs (and their TMEM) per SM
+                e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+            if (e != cudaSuccess)
+                return e;
+            if (dev >= 0 && dev < 64)
+                configured[dev] = true;
+        }
+    }
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(pkv::kTreeThreads), smem, st, mq, cm.k, cm.v,
+                               cm.k4, cm.v4, a);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned chunks = (unsigned)((std::min(a.max_query_len * a.group, pkv::kTreeRows) + 31) / 32);
+    return launch_pdl(pkv::tree_merge_kernel<D, BF16>, dim3((unsigned)ctas, chunks, (unsigned)a.shares), dim3(256),
+                      0, st, a);
+}
+
+template <bool BF16>
+cudaError_t dispatch_tree(int D, int bs, const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a,
+                          int ctas, cudaStream_t st)
+{
+    if (D == 64 && bs == 16) return launch_tree<64, 16, BF16>(mq, cm, a, ctas, st);
+    if (D == 64 && bs == 32) return launch_tree<64, 32, BF16>(mq, cm, a, ctas, st);
+    if (D == 128 && bs == 16) return launch_tree<128, 16, BF16>(mq, cm, a, ctas, st);
+    return launch_tree<128, 32, BF16>(mq, cm, a, ctas, st);
+}
+
+}  // namespace
+
 extern "C" size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_heads, int num_kv_heads,
                                            int head_dim, int max_blocks, int block_size)
 {
     if (check_shapes(batch, num_heads, num_kv_heads, head_dim, max_blocks, block_size) != PKV_OK ||
-        check_tree(0, max_query_len, batch) != PKV_OK)
+        check_tree(0, max_query_len, batch) != PKV_OK || batch == 0 || max_query_len == 0)
         return 0;
-    return 0;
+    return tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size).total;
 }
 
 extern "C" pkv_status pkv_paged_attention_tree(
@@ -1245,42 +1314,43 @@ extern "C" pkv_status pkv_paged_attention_tree(
         return fail(PKV_ERR_MISALIGNED, "query/cache/out pointers must be 16-byte aligned");
     if (!aligned4(query_start) || !aligned4(tree_mask) || !aligned4(block_tables) || !aligned4(context_lens))
         return fail(PKV_ERR_MISALIGNED, "query_start/tree_mask/block_tables/context_lens must be 4-byte aligned");
-    const size_t need = pkv_tree_workspace_bytes(batch, max_query_len, num_heads, num_kv_heads, head_dim,
-                                                 max_blocks, block_size);
-    if (need > 0) {
-        if (!workspace || workspace_bytes < need)
-            return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
-                        workspace ? workspace_bytes : (size_t)0);
-        if (!aligned16(workspace))
-            return fail(PKV_ERR_MISALIGNED, "workspace must be 16-byte aligned");
-    }
+    const TreePlan plan = tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size);
+    if (!workspace || workspace_bytes < plan.total)
+        return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.total,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (!aligned16(workspace))
+        return fail(PKV_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    const int group = num_heads / num_kv_heads;
+    CUtensorMap mq;
+    CacheMaps cm;
+    if ((s = make_query_map(&mq, query, num_tokens, num_heads, head_dim, group, pkv::kTreeRows / group, dtype)) != PKV_OK ||
+        (s = make_cache_maps(&cm, key_cache, value_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)) != PKV_OK)
+        return s;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
     pkv::TreeArgs a;
-    a.query = static_cast<const uint16_t *>(query);
     a.query_start = query_start;
     a.tree_mask = tree_mask;
-    a.key_cache = static_cast<const uint16_t *>(key_cache);
     a.value_cache = static_cast<const uint16_t *>(value_cache);
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.out = static_cast<uint16_t *>(out);
+    a.desc = reinterpret_cast<int4 *>(ws);
+    a.rec_ml = reinterpret_cast<float2 *>(ws + plan.ml);
+    a.rec_o = reinterpret_cast<float *>(ws + plan.o);
     a.batch = batch;
     a.num_tokens = num_tokens;
     a.max_query_len = max_query_len;
     a.words = (max_query_len + 31) / 32;
     a.max_blocks = max_blocks;
-    a.block_size = block_size;
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
-    a.group = num_heads / num_kv_heads;
+    a.group = group;
     a.num_blocks = (int)num_blocks;
+    a.shares = plan.shares;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    auto go = [&](auto kern) {
-        return launch_pdl(kern, dim3((unsigned)num_tokens, (unsigned)num_kv_heads), dim3(128), 0,
-                          static_cast<cudaStream_t>(stream), a);
-    };
-    const cudaError_t e =
-        head_dim == 64 ? (dtype == PKV_BF16 ? go(pkv::tree_attend_kernel<64, true>) : go(pkv::tree_attend_kernel<64, false>))
-                       : (dtype == PKV_BF16 ? go(pkv::tree_attend_kernel<128, true>) : go(pkv::tree_attend_kernel<128, false>));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == PKV_BF16 ? dispatch_tree<true>(head_dim, block_size, mq, cm, a, plan.ctas, st)
+                                            : dispatch_tree<false>(head_dim, block_size, mq, cm, a, plan.ctas, st);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_attend_kernel launch");
     return PKV_OK;
