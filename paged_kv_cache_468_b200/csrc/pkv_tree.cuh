@@ -379,15 +379,26 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     using Sh = TreeShape<D>;
     constexpr int KS = D / 16, KV_STEPS = kTreeKeys / 16, BPT = kTreeKeys / BS;
     constexpr uint32_t kTmemCols = 256;          // S/P: 2 x 64 columns, O: D columns at 128
+    // The tiles start on a 1024-byte boundary; what else the CTA keeps lies in
+    // whichever end of the 1024 bytes of slack has room (with 1 KB more two
+    // CTAs would not fit an SM).
+    struct Local {
+        uint64_t bars[Sh::kNumBars];
+        TreeWalk walk[2];
+        int64_t scan[kTreeThreads / 32];
+        uint32_t bad[2][4];
+        uint32_t tmem;
+    };
+    static_assert(sizeof(Local) <= 512, "fits one end of the slack");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[Sh::kNumBars];
-    __shared__ uint32_t s_tmem;
-    __shared__ TreeWalk s_walk[2];
-    __shared__ int64_t s_scan[kTreeThreads / 32];
-    __shared__ uint32_t s_bad[2][4];
-    const uint32_t data_s = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    uint8_t *data = smem_raw + (data_s - smem_addr(smem_raw));
-    const uint32_t bars_s = smem_addr(bars);
+    const uint32_t front = ((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw);
+    uint8_t *data = smem_raw + front;
+    const uint32_t data_s = smem_addr(data);
+    Local *loc = reinterpret_cast<Local *>(front >= 512u ? smem_raw : data + Sh::kDataBytes);
+    TreeWalk *s_walk = loc->walk;
+    int64_t *s_scan = loc->scan;
+    uint32_t(*s_bad)[4] = loc->bad;
+    const uint32_t bars_s = smem_addr(loc->bars);
     auto bar = [&](int i) { return bars_s + 8u * (uint32_t)i; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group, TT = kTreeRows / G, R = TT * G;
@@ -403,7 +414,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     fence_mbar_init();
     if (warp == 5) {
-        tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+        tmem_alloc(smem_addr(&loc->tmem), kTmemCols);
         tmem_relinquish();
     }
     // masked columns of a tile may meet V rows that no load has filled
@@ -418,7 +429,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_after();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&loc->tmem);
 
     // ---- this CTA's shares: a thread adds up a run of sequences, the block
     // their totals; the thread whose run holds the share's start finds it ----
