@@ -411,8 +411,8 @@ pkv_status pkv_draft_tree_mask(const int32_t *parents, int num_tokens, const int
  * (group size 1..8, head_dim 64 / 128, block_size 16 / 32); max_query_len <=
  * PKV_TREE_MAX_NODES, else PKV_ERR_UNSUPPORTED.
  */
-size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_heads, int num_kv_heads,
-                                int head_dim, int max_blocks, int block_size);
+size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_tokens, int num_heads,
+                                int num_kv_heads, int head_dim, int max_blocks, int block_size);
 pkv_status pkv_paged_attention_tree(const void *query, int num_tokens, const int32_t *query_start,
                                     int max_query_len, const int32_t *tree_mask,
                                     const void *key_cache, const void *value_cache,

@@ -1212,19 +1212,51 @@ namespace {
 
 // CTAs of a tree attention call and the layout of its records.
 struct TreePlan {
-    int ctas, shares;
-    size_t ml, o, total;        // workspace offsets; the descriptors come first
+    int few;                    // 16-row tiles per item of the few-rows kernel (1, 2), 0: the 128-row tiles
+    int part_tokens, parts;     // few rows: keys of a part, parts of the longest item
+    int ctas, shares;           // 128-row tiles
+    size_t ml, o, total;        // workspace offsets (128-row tiles: the descriptors come first)
 };
+#ifndef PKV_TUNE_FEW
+#define PKV_TUNE_FEW 32
+#endif
+#ifndef PKV_TUNE_PARTS
+#define PKV_TUNE_PARTS 592
+#endif
+#ifndef PKV_TUNE_MAXPART
+#define PKV_TUNE_MAXPART 512
+#endif
 TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
-                   int max_blocks, int block_size)
+                   int max_blocks, int block_size, int num_tokens)
 {
-    TreePlan p;
+    TreePlan p = {};
+    const int rows_per_item = max_query_len * (num_heads / num_kv_heads);
+    if (rows_per_item <= PKV_TUNE_FEW) {
+        p.few = rows_per_item <= 16 ? 1 : 2;
+        const int64_t span = (int64_t)max_blocks * block_size;
+        const int64_t items = (int64_t)batch * num_kv_heads;
+        int64_t parts = (PKV_TUNE_PARTS + items - 1) / items;           // enough CTAs
+        parts = std::max(parts, span >= 2048 ? (span + PKV_TUNE_MAXPART - 1) / PKV_TUNE_MAXPART : (int64_t)1);
+        const int64_t unit = std::max(64, block_size);
+        p.part_tokens = (int)(std::max<int64_t>(1, (span + parts * unit - 1) / (parts * unit)) * unit);
+        p.parts = (int)((span + p.part_tokens - 1) / p.part_tokens);
+        if (p.parts > 1) {
+            const size_t recs = (size_t)num_tokens * num_heads * p.parts;
+            p.o = align256(recs * sizeof(float2));
+            p.total = align256(p.o + recs * (size_t)head_dim * sizeof(float));
+        }
+        return p;
+    }
     const int per_tile = pkv::kTreeRows / (num_heads / num_kv_heads);
     const int row_tiles = (max_query_len + per_tile - 1) / per_tile;
     p.shares = row_tiles > 1 ? 2 : 1;
     // two CTAs per SM, fewer where the largest such call has less to share out
     const int64_t tiles = ((int64_t)max_blocks * block_size + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
     const int64_t units = (int64_t)batch * num_kv_heads * std::max(1, row_tiles) * (tiles + pkv::kTreeItemCost);
+    if (units >= (int64_t)1 << 31) {
+        p.ctas = 0;             // more than a call's shares are counted in
+        return p;
+    }
     p.ctas = (int)std::min<int64_t>(2 * kPlanSmCount, std::max<int64_t>(p.shares, units / pkv::kTreeMinUnits));
     p.ctas += p.ctas % p.shares;                // pairs
     const size_t rows = (size_t)p.ctas * 2 * 2 * pkv::kTreeRows;
@@ -1277,13 +1309,68 @@ cudaError_t dispatch_tree(int D, int bs, const CUtensorMap &mq, const CacheMaps 
 
 }  // namespace
 
-extern "C" size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_heads, int num_kv_heads,
-                                           int head_dim, int max_blocks, int block_size)
+namespace {
+
+// Warps and stages per warp of the few-rows kernel, as for the decode kernel.
+#ifndef PKV_TUNE_NW1
+#define PKV_TUNE_NW1 2
+#define PKV_TUNE_S1 2
+#endif
+#ifndef PKV_TUNE_NW2
+#define PKV_TUNE_NW2 2
+#define PKV_TUNE_S2 2
+#endif
+
+template <int D, int BS, bool BF16, int MT>
+cudaError_t launch_tree_rows(const CUtensorMap &mk, const CUtensorMap &mv, const pkv::TreeRowsArgs &a, int batch,
+                             cudaStream_t st)
+{
+    constexpr int NW = MT == 1 ? PKV_TUNE_NW1 : PKV_TUNE_NW2, S = MT == 1 ? PKV_TUNE_S1 : PKV_TUNE_S2;
+    constexpr int smem = pkv::TreeRowsShape<D, BS, MT, NW, S>::kSmemBytes;
+    auto kern = pkv::tree_rows_kernel<D, BS, BF16, MT, NW, S>;
+    static bool configured[64] = {};
+    static std::mutex mu;
+    const int dev = current_device();
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev < 0 || dev >= 64 || !configured[dev]) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess)
+                return e;
+            if (dev >= 0 && dev < 64)
+                configured[dev] = true;
+        }
+    }
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)a.num_parts, (unsigned)a.num_kv_heads, (unsigned)batch),
+                               dim3(NW * 32), smem, st, mk, mv, a);
+    if (e != cudaSuccess || a.num_parts == 1)
+        return e;
+    const unsigned eights = (unsigned)((a.max_query_len * a.group + 7) / 8);
+    return launch_pdl(pkv::tree_rows_merge_kernel<D, BF16>, dim3(eights, (unsigned)a.num_kv_heads, (unsigned)batch),
+                      dim3(256), 0, st, a, BS);
+}
+
+template <int D, int BS>
+cudaError_t dispatch_tree_rows(bool bf16, int mt, const CUtensorMap &mk, const CUtensorMap &mv,
+                               const pkv::TreeRowsArgs &a, int batch, cudaStream_t st)
+{
+    if (bf16)
+        return mt == 1 ? launch_tree_rows<D, BS, true, 1>(mk, mv, a, batch, st)
+                       : launch_tree_rows<D, BS, true, 2>(mk, mv, a, batch, st);
+    return mt == 1 ? launch_tree_rows<D, BS, false, 1>(mk, mv, a, batch, st)
+                   : launch_tree_rows<D, BS, false, 2>(mk, mv, a, batch, st);
+}
+
+}  // namespace
+
+extern "C" size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_tokens, int num_heads,
+                                           int num_kv_heads, int head_dim, int max_blocks, int block_size)
 {
     if (check_shapes(batch, num_heads, num_kv_heads, head_dim, max_blocks, block_size) != PKV_OK ||
-        check_tree(0, max_query_len, batch) != PKV_OK || batch == 0 || max_query_len == 0)
+        check_tree(num_tokens, max_query_len, batch) != PKV_OK || batch == 0 || max_query_len == 0 || num_tokens == 0)
         return 0;
-    return tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size).total;
+    return tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size, num_tokens)
+        .total;
 }
 
 extern "C" pkv_status pkv_paged_attention_tree(
@@ -1314,19 +1401,62 @@ extern "C" pkv_status pkv_paged_attention_tree(
         return fail(PKV_ERR_MISALIGNED, "query/cache/out pointers must be 16-byte aligned");
     if (!aligned4(query_start) || !aligned4(tree_mask) || !aligned4(block_tables) || !aligned4(context_lens))
         return fail(PKV_ERR_MISALIGNED, "query_start/tree_mask/block_tables/context_lens must be 4-byte aligned");
-    const TreePlan plan = tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size);
-    if (!workspace || workspace_bytes < plan.total)
+    const TreePlan plan =
+        tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size, num_tokens);
+    if (!plan.few && plan.ctas == 0)
+        return fail(PKV_ERR_UNSUPPORTED, "batch x num_kv_heads x row tiles x key tiles is 2^31 or more");
+    if (plan.total > 0 && (!workspace || workspace_bytes < plan.total))
         return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.total,
                     workspace ? workspace_bytes : (size_t)0);
-    if (!aligned16(workspace))
+    if (plan.total > 0 && !aligned16(workspace))
         return fail(PKV_ERR_MISALIGNED, "workspace must be 16-byte aligned");
     const int group = num_heads / num_kv_heads;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (plan.few) {
+        CUtensorMap mk, mv;
+        if ((s = make_cache_map(&mk, key_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)) != PKV_OK ||
+            (s = make_cache_map(&mv, value_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)) != PKV_OK)
+            return s;
+        pkv::TreeRowsArgs f;
+        f.query = static_cast<const uint16_t *>(query);
+        f.query_start = query_start;
+        f.tree_mask = tree_mask;
+        f.value_cache = static_cast<const uint16_t *>(value_cache);
+        f.block_tables = block_tables;
+        f.context_lens = context_lens;
+        f.out = static_cast<uint16_t *>(out);
+        f.rec_ml = reinterpret_cast<float2 *>(ws);
+        f.rec_o = reinterpret_cast<float *>(ws + plan.o);
+        f.num_tokens = num_tokens;
+        f.max_query_len = max_query_len;
+        f.words = (max_query_len + 31) / 32;
+        f.max_blocks = max_blocks;
+        f.num_heads = num_heads;
+        f.num_kv_heads = num_kv_heads;
+        f.group = group;
+        f.num_blocks = (int)num_blocks;
+        f.part_tokens = plan.part_tokens;
+        f.num_parts = plan.parts;
+        f.scale_log2 = scale_log2;
+        const bool bf = dtype == PKV_BF16;
+        const cudaError_t e =
+            head_dim == 64 ? (block_size == 16 ? dispatch_tree_rows<64, 16>(bf, plan.few, mk, mv, f, batch, st)
+                                               : dispatch_tree_rows<64, 32>(bf, plan.few, mk, mv, f, batch, st))
+                           : (block_size == 16 ? dispatch_tree_rows<128, 16>(bf, plan.few, mk, mv, f, batch, st)
+                                               : dispatch_tree_rows<128, 32>(bf, plan.few, mk, mv, f, batch, st));
+        if (e != cudaSuccess)
+            return cuda_fail(e, "tree_rows_kernel launch");
+        return PKV_OK;
+    }
+    const bool two_q = max_query_len * group <= 64;
     CUtensorMap mq;
     CacheMaps cm;
-    if ((s = make_query_map(&mq, query, num_tokens, num_heads, head_dim, group, pkv::kTreeRows / group, dtype)) != PKV_OK ||
+    if ((s = make_query_map(&mq, query, num_tokens, num_heads, head_dim, group,
+                            (two_q ? 64 : pkv::kTreeRows) / group, dtype)) != PKV_OK ||
         (s = make_cache_maps(&cm, key_cache, value_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)) != PKV_OK)
         return s;
-    unsigned char *ws = static_cast<unsigned char *>(workspace);
     pkv::TreeArgs a;
     a.query_start = query_start;
     a.tree_mask = tree_mask;
@@ -1347,8 +1477,8 @@ extern "C" pkv_status pkv_paged_attention_tree(
     a.group = group;
     a.num_blocks = (int)num_blocks;
     a.shares = plan.shares;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.q_slots = two_q ? 2 : 1;
+    a.scale_log2 = scale_log2;
     const cudaError_t e = dtype == PKV_BF16 ? dispatch_tree<true>(head_dim, block_size, mq, cm, a, plan.ctas, st)
                                             : dispatch_tree<false>(head_dim, block_size, mq, cm, a, plan.ctas, st);
     if (e != cudaSuccess)

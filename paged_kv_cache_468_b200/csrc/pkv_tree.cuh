@@ -227,6 +227,7 @@ struct TreeArgs {
     int group;
     int num_blocks;
     int shares;                      // 2: pairs of row tiles, then single ones; 1: single ones only
+    int q_slots;                     // 2: two Q buffers of 64 rows (no item has more), 1: one of 128
     float scale_log2;
 };
 
@@ -236,6 +237,9 @@ constexpr int kTreeKeys = 64;            // keys per tile
 constexpr int kTreeItemCost = 2;         // an item's start and end, in key tiles
 constexpr int kTreeMinUnits = 2;         // a CTA's share is not cut below this
 
+constexpr int kTreeParts = 6;            // queue of parts between a CTA's warps
+constexpr int kTreeScans = 8;            // masked tiles whose scan result is kept
+
 template <int D>
 struct TreeShape {
     static constexpr int kHalves = D / 64;
@@ -243,7 +247,7 @@ struct TreeShape {
     static constexpr int kKVHalf = kTreeKeys * 128;
     static constexpr int kQBytes = kHalves * kQHalf;
     static constexpr int kKVBytes = kHalves * kKVHalf;
-    // two CTAs per SM: 112 KB each (D = 128: 32 + 80, D = 64: 16 + 80)
+    // two CTAs per SM: 112 KB each for D = 128 (32 + 80), 96 KB for D = 64 (16 + 80)
     static constexpr int kKStages = D == 128 ? 3 : 6;
     static constexpr int kVStages = D == 128 ? 2 : 4;
     static constexpr int kKOff = kQBytes;
@@ -251,50 +255,50 @@ struct TreeShape {
     static constexpr int kDataBytes = kVOff + kVStages * kKVBytes;
     static constexpr int kSmemBytes = kDataBytes + 1024;
     // barriers
-    static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + kKStages, kVFull = kKEmpty + kKStages,
-                         kVEmpty = kVFull + kVStages, kSFull = kVEmpty + kVStages, kPFull = kSFull + 2,
-                         kODone = kPFull + 2, kDrain = kODone + 1, kScan = kDrain + 1, kNumBars = kScan + 1;
+    static constexpr int kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = kKFull + kKStages, kVFull = kKEmpty + kKStages,
+                         kVEmpty = kVFull + kVStages, kScanReq = kVEmpty + kVStages, kScanned = kScanReq + 1, kSFull = kScanned + 1,
+                         kPFull = kSFull + 2, kODone = kPFull + 2, kDrain = kODone + 1, kPartFull = kDrain + 1,
+                         kPartEmpty = kPartFull + kTreeParts, kNumBars = kPartEmpty + kTreeParts;
 };
 
-// One sequence of units: a share [g, end) of it, walked item by item.
-struct TreeSegment {
-    int b;            // sequence
-    int kvh;
-    int rt;           // row tile
+// A part of an item: key tiles k0 .. k1 - 1 of `tiles` for one row tile of a
+// (sequence, kv head).  k1 = 0 ends a CTA's parts.
+struct TreePart {
+    int b, kvh, rt, share;
     int q0, n, len;   // the sequence's rows and length
     int tiles;        // key tiles of the item
-    int k0, k1;       // this part's key tiles
+    int k0, k1;
 };
+// Units g .. end - 1 of a sequence of units, sequence b's first unit being seq0.
 struct TreeWalk {
-    int64_t g, end;   // units left
-    int64_t seq0;     // first unit of sequence b
-    int b;
+    int g, end, seq0, b;
 };
 
-// Units of a sequence: single items (pair = false) or pairs of row tiles.
-__device__ __forceinline__ int tree_items(int n, int G, bool single_only, bool pair)
+// Items of a sequence: single row tiles, or pairs of them.
+__device__ __forceinline__ int tree_items(int n, int G, int shares, int share)
 {
     const int tt = kTreeRows / G;
     const int rt = (n + tt - 1) / tt;
-    return pair ? rt / 2 : (single_only ? rt : rt & 1);
+    return shares == 1 ? rt : (share == 0 ? rt / 2 : rt & 1);
 }
-__device__ __forceinline__ int64_t tree_units(int items, int len, int kv_heads)
+// Units of sequence b (0 where it contradicts itself).  The host keeps the
+// total below 2^31.
+template <int BS>
+__device__ __forceinline__ int tree_units(const TreeArgs &a, int b, int share, TreeSeq *s)
 {
-    return (int64_t)items * kv_heads * ((len + kTreeKeys - 1) / kTreeKeys + kTreeItemCost);
+    if (!tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, s))
+        return -1;
+    return tree_items(s->n, a.group, a.shares, share) * a.num_kv_heads *
+           ((s->len + kTreeKeys - 1) / kTreeKeys + kTreeItemCost);
 }
 
 template <int BS>
-__device__ __forceinline__ bool tree_next(TreeWalk &w, const TreeArgs &a, int share, int member, TreeSegment *s)
+__device__ __forceinline__ bool tree_next(TreeWalk &w, const TreeArgs &a, int share, int member, TreePart *p)
 {
-    const bool pair = a.shares == 2 && share == 0;
     while (w.g < w.end) {
         TreeSeq q;
-        // contradicting sequences have no units
-        const bool ok = tree_seq(a.query_start, a.context_lens, w.b, a.num_tokens, a.max_query_len,
-                                 a.max_blocks * BS, &q);
-        const int items = ok ? tree_items(q.n, a.group, a.shares == 1, pair) : 0;
-        const int64_t units = tree_units(items, q.len, a.num_kv_heads);
-        const int64_t off = w.g - w.seq0;
+        const int units = max(0, tree_units<BS>(a, w.b, share, &q));
+        const int off = w.g - w.seq0;
         if (off >= units) {
             w.seq0 += units;
             ++w.b;
@@ -302,41 +306,45 @@ __device__ __forceinline__ bool tree_next(TreeWalk &w, const TreeArgs &a, int sh
         }
         const int tiles = (q.len + kTreeKeys - 1) / kTreeKeys;
         const int cost = tiles + kTreeItemCost;
-        const int item = (int)(off / cost);
-        const int k0 = (int)(off - (int64_t)item * cost);
-        const int step = (int)min((int64_t)(cost - k0), w.end - w.g);
+        const int item = off / cost;
+        const int k0 = off - item * cost;
+        const int step = min(cost - k0, w.end - w.g);
         w.g += step;
         if (k0 >= tiles)
             continue;
-        s->b = w.b;
-        s->kvh = item % a.num_kv_heads;
         const int r = item / a.num_kv_heads;
-        // pairs: row tiles 2 r and 2 r + 1; singles: row tile r, or the odd last one
-        s->rt = pair ? 2 * r + member : (a.shares == 1 ? r : (q.n + kTreeRows / a.group - 1) / (kTreeRows / a.group) - 1);
-        s->q0 = q.q0;
-        s->n = q.n;
-        s->len = q.len;
-        s->tiles = tiles;
-        s->k0 = k0;
-        s->k1 = min(tiles, k0 + step);
+        p->b = w.b;
+        p->kvh = item - r * a.num_kv_heads;
+        // pairs: row tiles 2 r and 2 r + 1; beside pairs, the odd last row tile
+        const int tt = kTreeRows / a.group;
+        p->rt = a.shares == 1 ? r : (share == 0 ? 2 * r + member : (q.n + tt - 1) / tt - 1);
+        p->share = share;
+        p->q0 = q.q0;
+        p->n = q.n;
+        p->len = q.len;
+        p->tiles = tiles;
+        p->k0 = k0;
+        p->k1 = min(tiles, k0 + step);
         return true;
     }
     return false;
 }
 
-__device__ __forceinline__ int64_t tree_cut(int64_t total, int c, int n)   // the first unit of CTA (or pair) c
+__device__ __forceinline__ int tree_cut(int total, int c, int n)   // the first unit of CTA (or pair) c of n
 {
-    return total / n * c + total % n * c / n;
+    const int q = total / n;
+    return q * c + (total - q * n) * c / n;
 }
-__device__ __forceinline__ int tree_ctas(int64_t total, int most)          // CTAs (or pairs) that share the units
+__device__ __forceinline__ int tree_ctas(int total, int most)      // CTAs (or pairs) that share the units
 {
-    const int64_t want = (total + kTreeMinUnits - 1) / kTreeMinUnits;
-    return (int)min((int64_t)most, max((int64_t)1, want));
+    return min(most, max(1, (total + kTreeMinUnits - 1) / kTreeMinUnits));
 }
 
 // Row r's visible positions p0 .. p0 + 63 as bits: committed cells, and the
 // drafted ones that its mask row names.
-__device__ __forceinline__ uint64_t tree_bits(const int32_t *mask, int words, int base, int n, int p0)
+// (mw: the row's first three words, read ahead).
+__device__ __forceinline__ uint64_t tree_bits(const int32_t *mask, const uint32_t (&mw)[3], int words, int base,
+                                              int n, int p0)
 {
     int j0 = p0 - base;
     uint64_t ones = 0ull;
@@ -352,9 +360,12 @@ __device__ __forceinline__ uint64_t tree_bits(const int32_t *mask, int words, in
     if (left <= 0)
         return ones;
     const int w = j0 >> 5, o = j0 & 31;
-    const uint32_t w0 = (uint32_t)__ldg(mask + w);
-    const uint32_t w1 = w + 1 < words ? (uint32_t)__ldg(mask + w + 1) : 0u;
-    const uint32_t w2 = w + 2 < words ? (uint32_t)__ldg(mask + w + 2) : 0u;
+    uint32_t w0 = mw[0], w1 = mw[1], w2 = mw[2];
+    if (w > 0) {
+        w0 = (uint32_t)__ldg(mask + w);
+        w1 = w + 1 < words ? (uint32_t)__ldg(mask + w + 1) : 0u;
+        w2 = w + 2 < words ? (uint32_t)__ldg(mask + w + 2) : 0u;
+    }
     uint64_t v = (uint64_t)__funnelshift_r(w0, w1, o) | ((uint64_t)__funnelshift_r(w1, w2, o) << 32);
     if (left < 64)
         v &= (1ull << left) - 1ull;
@@ -370,42 +381,93 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x)   // bit 0: low half,
     return ((y & 0xffffu) == (e & 0xffffu) ? 1u : 0u) | ((y >> 16) == (e >> 16) ? 0x10000u : 0u);
 }
 
+// O_row += the infinities and NaN of V's rows of key tile t that the row sees
+// (they were zeroed in shared memory).  Rare, so simple: one key at a time,
+// read from the cache again.
+template <int D, int BS, bool BF16>
+__device__ __noinline__ void tree_add_nonfinite(const TreeArgs &a, const TreePart &s, int t, uint64_t vis, uint32_t tO)
+{
+    const int nblk = (s.len + BS - 1) / BS, tail = s.len % BS;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c0, o);
+#pragma unroll 1
+        for (int c = 0; c < kTreeKeys; ++c) {
+            const int bi = t * (kTreeKeys / BS) + c / BS;
+            if (bi >= nblk)
+                break;
+            const int cell = c % BS - (tail && bi == nblk - 1 ? BS - tail : 0);
+            if (cell < 0)
+                continue;
+            int blk = __ldg(a.block_tables + (size_t)s.b * a.max_blocks + bi);
+            blk = (unsigned)blk < (unsigned)a.num_blocks ? blk : 0;
+            const uint32_t *v = reinterpret_cast<const uint32_t *>(
+                a.value_cache + (((size_t)blk * BS + cell) * a.num_kv_heads + s.kvh) * D + c0);
+            const bool see = (vis >> c) & 1ull;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t x = __ldg(v + i);
+                const uint32_t f = nonfinite2<BF16>(x);
+                const float2 y = unpack2<BF16>(x);
+                if (see && (f & 1u))
+                    o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) + y.x);
+                if (see && (f >> 16))
+                    o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) + y.y);
+            }
+        }
+        tmem_st32(tO + c0, o);
+    }
+    tmem_wait_st();
+}
+
+// Warps: 0-3 softmax and output (warp w owns TMEM lanes 32 w ..), 4 K loads,
+// 5 MMA issue, 6 V loads, 7 the parts' queue, Q loads and the scan of masked
+// tiles' V rows.
 template <int D, int BS, bool BF16>
 __global__ void __launch_bounds__(kTreeThreads, 2)
 tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k4,
-                   const __grid_constant__ CUtensorMap tm_v4, const TreeArgs a)
+                   const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ TreeArgs a)
 {
     using Sh = TreeShape<D>;
     constexpr int KS = D / 16, KV_STEPS = kTreeKeys / 16, BPT = kTreeKeys / BS;
     constexpr uint32_t kTmemCols = 256;          // S/P: 2 x 64 columns, O: D columns at 128
-    // The tiles start on a 1024-byte boundary; what else the CTA keeps lies in
-    // whichever end of the 1024 bytes of slack has room (with 1 KB more two
-    // CTAs would not fit an SM).
+    // The dynamic shared memory is all that the kernel has, so it starts on the
+    // 1024-byte boundary that the swizzled tiles need; what else the CTA keeps
+    // follows them (with 1 KB more two CTAs would not fit an SM).
     struct Local {
         uint64_t bars[Sh::kNumBars];
         TreeWalk walk[2];
-        int64_t scan[kTreeThreads / 32];
-        uint32_t bad[2][4];
+        int total[2];
+        int scan[kTreeThreads / 32];
+        uint32_t bad[kTreeScans];
         uint32_t tmem;
+        TreePart part[kTreeParts];
     };
-    static_assert(sizeof(Local) <= 512, "fits one end of the slack");
+    static_assert(sizeof(Local) <= 1024, "fits behind the tiles");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t front = ((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw);
-    uint8_t *data = smem_raw + front;
+    uint8_t *data = smem_raw;
     const uint32_t data_s = smem_addr(data);
-    Local *loc = reinterpret_cast<Local *>(front >= 512u ? smem_raw : data + Sh::kDataBytes);
-    TreeWalk *s_walk = loc->walk;
-    int64_t *s_scan = loc->scan;
-    uint32_t(*s_bad)[4] = loc->bad;
+    Local *loc = reinterpret_cast<Local *>(data + Sh::kDataBytes);
+    TreePart *s_part = loc->part;
+    if (data_s & 1023u) {                            // (never seen: fail loudly, not by wrong tiles)
+        if (threadIdx.x == 0)
+            raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+        return;
+    }
     const uint32_t bars_s = smem_addr(loc->bars);
     auto bar = [&](int i) { return bars_s + 8u * (uint32_t)i; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group, TT = kTreeRows / G, R = TT * G;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < Sh::kNumBars; ++i)
-            mbar_init(bar(i), i == Sh::kPFull || i == Sh::kPFull + 1 || i == Sh::kScan ? 4 : 1);
+    if (threadIdx.x < Sh::kNumBars) {
+        const int i = threadIdx.x;
+        // P: one arrival per softmax warp; a part is read by K, V and MMA warps and the softmax warps
+        const int count = i >= Sh::kPFull && i < Sh::kPFull + 2 ? 4 : (i >= Sh::kPartEmpty ? 7 : 1);
+        mbar_init(bar(i), count);
+    }
+    if (threadIdx.x == 128) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -424,12 +486,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             vr[i] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&loc->tmem);
 
     // ---- this CTA's shares: a thread adds up a run of sequences, the block
     // their totals; the thread whose run holds the share's start finds it ----
@@ -437,99 +495,87 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool pair = a.shares == 2 && share == 0;
         const int per = (a.batch + kTreeThreads - 1) / kTreeThreads;
         const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-        int64_t mine = 0;
+        int mine = 0;
         for (int b = b0; b < b1; ++b) {
             TreeSeq q;
-            if (tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &q))
-                mine += tree_units(tree_items(q.n, G, a.shares == 1, pair), q.len, a.num_kv_heads);
-            else if (blockIdx.x == 0 && share == 0)
+            const int u = tree_units<BS>(a, b, share, &q);
+            if (u < 0 && blockIdx.x == 0 && share == 0)
                 raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
+            mine += max(u, 0);
         }
-        int64_t upto = mine;                         // inclusive prefix over the block
+        int upto = mine;                             // inclusive prefix over the block
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o)
                 upto += x;
         }
         if (lane == 31)
-            s_scan[warp] = upto;
+            loc->scan[warp] = upto;
+        if (threadIdx.x == 0)
+            loc->walk[share] = TreeWalk{0, 0, 0, 0}; // an empty share
         __syncthreads();
-        int64_t total = 0;
+        int total = 0;
 #pragma unroll
         for (int i = 0; i < kTreeThreads / 32; ++i) {
+            const int x = loc->scan[i];
             if (i < warp)
-                upto += s_scan[i];
-            total += s_scan[i];
+                upto += x;
+            total += x;
         }
         const int n = tree_ctas(total, pair ? gridDim.x / 2 : gridDim.x);
         const int c = pair ? blockIdx.x >> 1 : blockIdx.x;
-        const int64_t g0 = c < n ? tree_cut(total, c, n) : total;
-        const int64_t g1 = c < n ? tree_cut(total, c + 1, n) : total;
-        if (threadIdx.x == 0)
-            s_walk[share] = TreeWalk{0, 0, 0, 0};    // an empty share
-        __syncthreads();
-        if (g0 < g1 && g0 >= upto - mine && g0 < upto) {
-            int64_t at = upto - mine;
-            int b = b0;
+        const int g0 = c < n ? tree_cut(total, c, n) : total;
+        if (g0 >= upto - mine && g0 < upto) {
+            int at = upto - mine, b = b0;
             for (;; ++b) {
                 TreeSeq q;
-                int64_t u = 0;
-                if (tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &q))
-                    u = tree_units(tree_items(q.n, G, a.shares == 1, pair), q.len, a.num_kv_heads);
+                const int u = max(0, tree_units<BS>(a, b, share, &q));
                 if (g0 < at + u)
                     break;
                 at += u;
             }
-            s_walk[share] = TreeWalk{g0, g1, at, b};
+            loc->walk[share] = TreeWalk{g0, tree_cut(total, c + 1, n), at, b};
         }
+        if (threadIdx.x == 0)
+            loc->total[share] = total;
+        tc_fence_before();
         __syncthreads();
-        if (threadIdx.x == 0) {
-            // An item that started in the share before and goes on here: its
-            // second part.  The merge finds the item's records through it.
-            int4 d = make_int4(0, 0, 0, 0);
-            TreeWalk w = s_walk[share];
-            TreeSeq q;
-            if (c > 0 && w.g < w.end &&
-                tree_seq(a.query_start, a.context_lens, w.b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &q)) {
-                const int tiles = (q.len + kTreeKeys - 1) / kTreeKeys;
-                const int k0 = (int)((w.g - w.seq0) % (tiles + kTreeItemCost));
-                const int64_t start = w.g - k0;      // the item's first unit
-                TreeSegment s;
-                if (k0 > 0 && k0 < tiles && start >= tree_cut(total, c - 1, n) &&
-                    tree_next<BS>(w, a, share, blockIdx.x & 1, &s)) {
-                    int last = c;                    // the last CTA (or pair) with keys of the item
-                    while (last + 1 < n && tree_cut(total, last + 1, n) < start + tiles)
-                        ++last;
-                    d = make_int4(s.q0 + s.rt * TT, min(R, s.n * G - s.rt * R), s.kvh, last - c + 2);
-                }
-            }
-            a.desc[blockIdx.x * 2 + share] = d;
-        }
+        tc_fence_after();
     }
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&loc->tmem);
 
     const uint32_t sQ = data_s, sK = data_s + Sh::kKOff, sV = data_s + Sh::kVOff;
     const uint32_t tO = tmem + 2 * kTreeKeys;
-    const int member = blockIdx.x & 1;
+    const bool two_q = a.q_slots == 2;               // at most 64 rows: two Q buffers of 64 rows
 
-    // every role walks the same parts; key tiles are numbered on across them (J)
-    int w_share = 0;
-    TreeWalk walk = s_walk[0];
-    auto next_part = [&](TreeSegment *s) -> bool {
-        for (;;) {
-            if (tree_next<BS>(walk, a, w_share, member, s))
-                return true;
-            if (++w_share >= a.shares)
-                return false;
-            walk = s_walk[w_share];
+    // The parts in order, from the queue that warp 7 fills (used by whole
+    // warps, or by one thread with one = true); false at their end.
+    int part_i = 0;
+    auto next_part = [&](TreePart *p, bool one) -> bool {
+        const int slot = part_i % kTreeParts;
+        bool got = mbar_wait_bounded(bar(Sh::kPartFull + slot), (uint32_t)((part_i / kTreeParts) & 1), kWaitLimitNs);
+        if (!one)
+            got = __all_sync(0xffffffffu, got);
+        if (!got) {
+            if (one || lane == 0)
+                raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+            return false;
         }
+        *p = s_part[slot];
+        if (!one)
+            __syncwarp();
+        if (one || lane == 0)
+            mbar_arrive(bar(Sh::kPartEmpty + slot));
+        ++part_i;
+        return p->k1 > 0;
     };
 
     if (warp == 4 || warp == 6) {
         // ---- loads: warp 4 the K ring, warp 6 the V ring ----
         const bool is_k = warp == 4;
-        const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
-        const CUtensorMap *tm4 = is_k ? &tm_k4 : &tm_v4;
+        const CUtensorMap *tm = is_k ? &tm_k : &tm_v;        // 3-D view: whole blocks
+        const CUtensorMap *tm4 = is_k ? &tm_k4 : &tm_v4;     // 4-D view: shifted last blocks
         const int full0 = is_k ? Sh::kKFull : Sh::kVFull;
         const int empty0 = is_k ? Sh::kKEmpty : Sh::kVEmpty;
         const uint32_t ring = is_k ? sK : sV;
@@ -537,26 +583,27 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint64_t once = policy_evict_first(), again = policy_evict_normal();
         int J = 0, st = 0, round = 0;
         bool ok = true;
-        TreeSegment s;
-        while (ok && next_part(&s)) {
-            const uint64_t policy = a.shares == 2 && w_share == 0 ? again : once;
+        TreePart s;
+        while (ok && next_part(&s, false)) {
+            // a pair's keys are read a second time, by the other CTA
+            const uint64_t policy = a.shares == 2 && s.share == 0 ? again : once;
             const int nblk = (s.len + BS - 1) / BS;
             const int tail = s.len % BS;
             const int32_t *trow = a.block_tables + (size_t)s.b * a.max_blocks;
             int ids = 0, have = -1;                  // block ids of the 32-entry window `have`
             for (int t = s.k0; t < s.k1; ++t, ++J) {
+                const int kb0 = t * BPT;             // a tile's ids lie in one window
+                const int nb = min(BPT, nblk - kb0);
+                if ((kb0 & ~31) != have) {
+                    have = kb0 & ~31;
+                    ids = have + lane < nblk ? __ldg(trow + have + lane) : 0;
+                }
                 if (J >= NS) {
                     const bool free_ = mbar_wait_bounded(bar(empty0 + st), (uint32_t)((round - 1) & 1), kWaitLimitNs);
                     if (!__all_sync(0xffffffffu, free_)) {
                         ok = false;
                         break;
                     }
-                }
-                const int kb0 = t * BPT;             // a tile's ids lie in one window
-                const int nb = min(BPT, nblk - kb0);
-                if ((kb0 & ~31) != have) {
-                    have = kb0 & ~31;
-                    ids = have + lane < nblk ? __ldg(trow + have + lane) : 0;
                 }
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar(full0 + st), (uint32_t)(nb * BS * D * 2));
@@ -589,74 +636,214 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (lane == 0)
             for (int j = J > NS ? J - NS : 0; j < J; ++j)
                 mbar_wait_bounded(bar(full0 + j % NS), (uint32_t)((j / NS) & 1), kWaitLimitNs / 8);
+        if (is_k && lane < a.shares) {
+            // An item that started in the share before and goes on in this one:
+            // the merge finds its records through this share.
+            const int share = lane;
+            const bool pair = a.shares == 2 && share == 0;
+            const int total = loc->total[share];
+            const int n = tree_ctas(total, pair ? gridDim.x / 2 : gridDim.x);
+            const int c = pair ? blockIdx.x >> 1 : blockIdx.x;
+            int4 d = make_int4(0, 0, 0, 0);
+            TreeWalk w = loc->walk[share];
+            TreeSeq q;
+            if (c > 0 && w.g < w.end && tree_units<BS>(a, w.b, share, &q) > 0) {
+                const int tiles = (q.len + kTreeKeys - 1) / kTreeKeys;
+                const int k0 = (w.g - w.seq0) % (tiles + kTreeItemCost);
+                const int start = w.g - k0;          // the item's first unit
+                TreePart p;
+                if (k0 > 0 && k0 < tiles && start >= tree_cut(total, c - 1, n) &&
+                    tree_next<BS>(w, a, share, blockIdx.x & 1, &p)) {
+                    int last = c;                    // the last CTA (or pair) with keys of the item
+                    while (last + 1 < n && tree_cut(total, last + 1, n) < start + tiles)
+                        ++last;
+                    d = make_int4(p.q0 + p.rt * TT, min(R, p.n * G - p.rt * R), p.kvh, last - c + 2);
+                }
+            }
+            a.desc[blockIdx.x * 2 + share] = d;
+        }
     } else if (warp == 7) {
-        // ---- Q of each part, once the previous part's last S has completed ----
-        if (lane == 0) {
-            const uint64_t policy = policy_evict_normal();
-            TreeSegment s;
-            int u = 0;
-            while (next_part(&s)) {
-                if (u > 0 && !mbar_wait_bounded(bar(Sh::kQEmpty), (uint32_t)((u - 1) & 1), kWaitLimitNs)) {
-                    raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+        // ---- the queue, Q, and the scan of masked tiles ----
+        // Parts are queued up to four ahead of the one whose tiles are scanned
+        // here: the loaders run at most their rings ahead of the MMAs.
+        constexpr int kAhead = 4;
+        const uint64_t policy = policy_evict_normal();
+        TreeWalk walk = loc->walk[0];
+        int share = 0, made = 0, scans = 0, vs = 0, vround = 0;
+        bool ok = true, done = false;
+        auto make = [&]() {                          // queue part `made`
+            const int slot = made % kTreeParts;
+            if (made >= kTreeParts &&
+                !__all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kPartEmpty + slot),
+                                                           (uint32_t)((made / kTreeParts - 1) & 1), kWaitLimitNs))) {
+                ok = false;
+                return;
+            }
+            TreePart p;
+            while (!tree_next<BS>(walk, a, share, blockIdx.x & 1, &p)) {
+                if (++share >= a.shares) {
+                    done = true;
+                    p.k1 = 0;
                     break;
                 }
-                mbar_arrive_expect_tx(bar(Sh::kQFull), (uint32_t)(Sh::kHalves * R * 128));
+                walk = loc->walk[share];
+            }
+            if (lane == 0) {
+                s_part[slot] = p;
+                mbar_arrive(bar(Sh::kPartFull + slot));
+            }
+            __syncwarp();
+            ++made;
+        };
+        auto load_q = [&](int u, const TreePart &p) {
+            const int slot = two_q ? u & 1 : 0;
+            const int turn = two_q ? u >> 1 : u;
+            if (turn > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kQEmpty + slot), (uint32_t)((turn - 1) & 1),
+                                                                       kWaitLimitNs))) {
+                ok = false;
+                return;
+            }
+            if (lane == 0) {
+                const int rows = (two_q ? 64 / G : TT) * G;
+                mbar_arrive_expect_tx(bar(Sh::kQFull + slot), (uint32_t)(Sh::kHalves * rows * 128));
 #pragma unroll
                 for (int h = 0; h < Sh::kHalves; ++h)
-                    tma_load_3d(sQ + h * Sh::kQHalf, &tm_q, bar(Sh::kQFull), h * 64, s.kvh * G, s.q0 + s.rt * TT, policy);
-                ++u;
+                    tma_load_3d(sQ + h * Sh::kQHalf + slot * 64 * 128, &tm_q, bar(Sh::kQFull + slot), h * 64, p.kvh * G,
+                                p.q0 + p.rt * TT, policy);
             }
-            if (u > 0)
-                mbar_wait_bounded(bar(Sh::kQFull), (uint32_t)((u - 1) & 1), kWaitLimitNs / 8);
+            __syncwarp();
+        };
+        int u = 0, loaded = 0;                       // part scanned; Q loads issued
+        while (ok) {
+            while (ok && !done && made <= u + kAhead)
+                make();
+            if (!ok)
+                break;
+            const TreePart s = s_part[u % kTreeParts];   // (rewritten only by this warp, when made reaches u + kTreeParts)
+            if (s.k1 == 0)
+                break;
+            if (loaded == u) {
+                load_q(u, s);
+                ++loaded;
+            }
+            if (two_q && ok) {
+                const TreePart nx = s_part[(u + 1) % kTreeParts];   // made > u + 1, or the end marker
+                if (nx.k1 > 0) {
+                    load_q(u + 1, nx);
+                    ++loaded;
+                }
+            }
+            for (int t = s.k0; ok && t < s.k1; ++t) {
+                if ((t + 1) * kTreeKeys > s.len - s.n) {
+                    // the MMA thread asks for it when the tile's V has landed: this
+                    // warp's place in the tiles says nothing of the V ring's
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kScanReq), (uint32_t)(scans & 1), kWaitLimitNs) &&
+                                                        mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs))) {
+                        ok = false;
+                        break;
+                    }
+                    uint4 *vt = reinterpret_cast<uint4 *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
+                    uint32_t any = 0u;
+#pragma unroll 8
+                    for (int i = 0; i < Sh::kKVBytes / 512; ++i) {
+                        const uint4 x = vt[i * 32];
+                        any |= nonfinite2<BF16>(x.x) | nonfinite2<BF16>(x.y) | nonfinite2<BF16>(x.z) | nonfinite2<BF16>(x.w);
+                    }
+                    const bool bad = __any_sync(0xffffffffu, any != 0u);
+                    if (bad) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
+#pragma unroll 1
+                        for (int i = 0; i < Sh::kKVBytes / 128; ++i)
+                            w[i * 32] &= ~(nonfinite2<BF16>(w[i * 32]) * 0xffffu);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        loc->bad[scans % kTreeScans] = bad;
+                        mbar_arrive(bar(Sh::kScanned));
+                    }
+                    ++scans;
+                }
+                if (++vs == Sh::kVStages) {
+                    vs = 0;
+                    ++vround;
+                }
+            }
+            ++u;
         }
+        if (!ok && lane == 0)
+            raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+        // the last Q loads land before the CTA can exit
+        if (lane == 0)
+            for (int i = max(0, loaded - (two_q ? 2 : 1)); i < loaded; ++i)
+                mbar_wait_bounded(bar(Sh::kQFull + (two_q ? i & 1 : 0)), (uint32_t)((two_q ? i >> 1 : i) & 1), kWaitLimitNs / 8);
     } else if (warp == 5) {
         // ---- MMA issue: one thread ----
         if (lane == 0) {
             constexpr uint32_t idS = f16_idesc<BF16>(kTreeRows, kTreeKeys, false);
             constexpr uint32_t idO = f16_idesc<BF16>(kTreeRows, D, true);
             int ks_ = 0, kround = 0;                 // K stage of the next S
-            auto issue_s = [&](int J) -> bool {
+            // S of global tile J; u: its part (Q buffer); last: the part's last S
+            auto issue_s = [&](int J, int u, bool last) -> bool {
                 if (!mbar_wait_bounded(bar(Sh::kKFull + ks_), (uint32_t)(kround & 1), kWaitLimitNs))
                     return false;
                 tc_fence_after();
                 const uint32_t kt = sK + ks_ * Sh::kKVBytes;
+                // with two Q buffers the rows past a buffer's 64 read what lies
+                // behind it: rows that nobody reads
+                const uint32_t qt = sQ + (two_q ? (u & 1) * 64 * 128 : 0);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint32_t koff = (uint32_t)((ks & 3) * 32);
-                    tc_mma_f16(tmem + (J & 1) * kTreeKeys, sw128_desc(sQ + (ks >> 2) * Sh::kQHalf + koff, 16, 1024),
+                    tc_mma_f16(tmem + (J & 1) * kTreeKeys, sw128_desc(qt + (ks >> 2) * Sh::kQHalf + koff, 16, 1024),
                                sw128_desc(kt + (ks >> 2) * Sh::kKVHalf + koff, 16, 1024), idS, ks > 0 ? 1u : 0u);
                 }
                 tc_commit(bar(Sh::kSFull + (J & 1)));
                 tc_commit(bar(Sh::kKEmpty + ks_));
+                if (last)
+                    tc_commit(bar(Sh::kQEmpty + (two_q ? u & 1 : 0)));
                 if (++ks_ == Sh::kKStages) {
                     ks_ = 0;
                     ++kround;
                 }
                 return true;
             };
-            TreeSegment s, nx;
-            bool has = next_part(&s), has_nx = has && next_part(&nx);
+            auto q_ready = [&](int u) -> bool {
+                return mbar_wait_bounded(bar(Sh::kQFull + (two_q ? u & 1 : 0)), (uint32_t)((two_q ? u >> 1 : u) & 1),
+                                         kWaitLimitNs);
+            };
+            TreePart s, nx;
+            bool has = next_part(&s, true), has_nx = has && next_part(&nx, true);
             bool ok = true;
             int J = 0, u = 0, vs = 0, vround = 0;
-            if (has) {
-                ok = mbar_wait_bounded(bar(Sh::kQFull), 0u, kWaitLimitNs) && issue_s(0);
-                if (ok && s.k1 - s.k0 == 1)
-                    tc_commit(bar(Sh::kQEmpty));     // the part's last S
-            }
+            int scans = 0;
+            if (has)
+                ok = q_ready(0) && issue_s(0, 0, s.k1 - s.k0 == 1);
             while (ok && has) {
                 const int cnt = s.k1 - s.k0;
+                const int first_masked = (s.len - s.n) / kTreeKeys - s.k0;   // (tiles of this part)
                 for (int j = 0; j < cnt; ++j, ++J) {
-                    if (j + 1 < cnt) {
-                        // S_{J+1} overwrites the buffer that P_{J-1} V_{J-1} reads
+                    const bool last = j + 1 == cnt;
+                    // The next S, of this part or the next one, before this
+                    // tile's P V: it overwrites the buffer that P_{J-1} V_{J-1}
+                    // reads.  With one Q buffer the next part's first S comes
+                    // after P V: its Q may still be on the way.
+                    if (!last || (has_nx && two_q)) {
                         if (J >= 1 && !(ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs)))
                             break;
-                        if (!(ok = issue_s(J + 1)))
+                        ok = last ? q_ready(u + 1) && issue_s(J + 1, u + 1, nx.k1 - nx.k0 == 1)
+                                  : issue_s(J + 1, u, j + 2 == cnt);
+                        if (!ok)
                             break;
-                        if (j + 2 == cnt)
-                            tc_commit(bar(Sh::kQEmpty));
                     }
-                    ok = mbar_wait_bounded(bar(Sh::kPFull + (J & 1)), (uint32_t)((J >> 1) & 1), kWaitLimitNs) &&
-                         mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs);
+                    // a masked tile's V rows are scanned (warp 7) while the softmax works
+                    ok = mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs);
+                    if (ok && j >= first_masked) {
+                        mbar_arrive(bar(Sh::kScanReq));
+                        ok = mbar_wait_bounded(bar(Sh::kScanned), (uint32_t)(scans & 1), kWaitLimitNs);
+                        ++scans;
+                    }
+                    ok = ok && mbar_wait_bounded(bar(Sh::kPFull + (J & 1)), (uint32_t)((J >> 1) & 1), kWaitLimitNs);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -672,22 +859,20 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         vs = 0;
                         ++vround;
                     }
+                    if (last && has_nx && !two_q) {
+                        // O_DONE of this tile: it completes after the MMAs that read
+                        // the buffer, and a wait for the phase before could miss it
+                        if (!(ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)(J & 1), kWaitLimitNs) && q_ready(u + 1) &&
+                                   issue_s(J + 1, u + 1, nx.k1 - nx.k0 == 1)))
+                            break;
+                    }
                 }
                 if (!ok)
                     break;
-                if (has_nx) {
-                    // the next part's first S: its buffer was read by P_{J-2} V_{J-2},
-                    // which completed before P_{J-1} V_{J-1} (waited for here)
-                    if (!(ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs) &&
-                               mbar_wait_bounded(bar(Sh::kQFull), (uint32_t)((u + 1) & 1), kWaitLimitNs) && issue_s(J)))
-                        break;
-                    ++u;
-                    if (nx.k1 - nx.k0 == 1)
-                        tc_commit(bar(Sh::kQEmpty));
-                }
+                ++u;
                 s = nx;
                 has = has_nx;
-                has_nx = has && next_part(&nx);
+                has_nx = has && next_part(&nx, true);
             }
             if (!ok)
                 raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
@@ -709,80 +894,45 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool fold = sc > 0.f;                  // a positive scale joins the exponent's fma
         const float sm = fold ? 1.f : sc, se = fold ? sc : 1.f;
         bool ok = true;
-        int J = 0, scans = 0, vs = 0, vround = 0;
-        TreeSegment s;
-        while (ok && next_part(&s)) {
+        int J = 0, scans = 0;
+        TreePart s;
+        while (ok && next_part(&s, false)) {
             const int rows = min(R, s.n * G - s.rt * R);      // rows of this tile
             const bool warp_on = warp * 32 < rows;
             const bool real = r < rows;
-            const int tok = s.q0 + s.rt * TT + (real ? r_tok : 0);   // this row's node
             const int base = s.len - s.n;
             const int tail = s.len % BS;
+            const int32_t *mrow = a.tree_mask + (size_t)(s.q0 + s.rt * TT + (real ? r_tok : 0)) * a.words;
+            // the row's first mask words, long before the masked tiles come
+            uint32_t mw[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                mw[i] = i < a.words ? (uint32_t)__ldg(mrow + i) : 0u;
             float m_used = kNegInf, l = 0.f;
+            uint64_t vis = 0ull;                     // of the last masked tile
+            bool was_masked = false;
+            // after P V of tile t - 1 (or the last one): what the scan took out of its V
+            auto mend = [&](int t) {
+                if (was_masked && *reinterpret_cast<volatile uint32_t *>(&loc->bad[(scans - 1) % kTreeScans])) {
+                    if (warp_on)
+                        tree_add_nonfinite<D, BS, BF16>(a, s, t, real ? vis : 0ull, tO + lane_base);
+                    __syncwarp();
+                }
+            };
             for (int t = s.k0; t < s.k1; ++t, ++J) {
                 const int t0 = t * kTreeKeys;
                 const int sb = J & 1;
                 const bool masked = t0 + kTreeKeys > base;
-                uint64_t vis = ~0ull;
-                if (masked) {
-                    vis = tree_bits(a.tree_mask + (size_t)tok * a.words, a.words, base, s.n, t0);
-                    if (t + 1 == s.tiles && tail) {
-                        // the partly filled last block was loaded to end its slot
-                        const int lo = s.len - tail - t0;
-                        const uint64_t low = (1ull << lo) - 1ull;
-                        vis = (vis & low) | ((vis & ~low) << (BS - tail));
-                    }
-                }
                 ok = mbar_wait_bounded(bar(Sh::kSFull + sb), (uint32_t)((J >> 1) & 1), kWaitLimitNs);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                bool bad = false;                    // the tile's V holds an infinity or a NaN
-                if (masked) {
-                    ok = mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    uint4 *vt = reinterpret_cast<uint4 *>(data + Sh::kVOff + vs * Sh::kKVBytes);
-                    uint32_t any = 0u;
-#pragma unroll
-                    for (int i = 0; i < Sh::kKVBytes / 16 / 128; ++i) {
-                        const uint4 x = vt[i * 128 + r];
-                        any |= nonfinite2<BF16>(x.x) | nonfinite2<BF16>(x.y) | nonfinite2<BF16>(x.z) | nonfinite2<BF16>(x.w);
-                    }
-                    const bool here = __any_sync(0xffffffffu, any != 0u);
-                    if (lane == 0) {
-                        s_bad[scans & 1][warp] = here;
-                        mbar_arrive(bar(Sh::kScan));
-                    }
-                    ok = mbar_wait_bounded(bar(Sh::kScan), (uint32_t)(scans & 1), kWaitLimitNs);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    const volatile uint32_t *sb4 = s_bad[scans & 1];
-                    bad = (sb4[0] | sb4[1] | sb4[2] | sb4[3]) != 0u;
-                    ++scans;
-                    if (here) {
-#pragma unroll 1
-                        for (int i = 0; i < Sh::kKVBytes / 16 / 128; ++i) {
-                            uint4 x = vt[i * 128 + r];
-                            uint32_t *w = &x.x;
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t f = nonfinite2<BF16>(w[e]);
-                                w[e] &= ~(f * 0xffffu);
-                            }
-                            vt[i * 128 + r] = x;
-                        }
-                        fence_proxy_async_smem();
-                    }
-                }
                 bool resc = false;
                 float alpha = 1.f;
                 uint32_t pk[32];
+                uint64_t vis_now = ~0ull;
                 if (warp_on) {
                     uint32_t raw[64];
                     tmem_ld64(tmem + lane_base + sb * kTreeKeys, raw);
@@ -791,7 +941,14 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int c = 0; c < 64; ++c)
                         x[c] = fold ? __uint_as_float(raw[c]) : __uint_as_float(raw[c]) * sm;
                     if (masked) {
-                        const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
+                        vis_now = tree_bits(mrow, mw, a.words, base, s.n, t0);
+                        if (t + 1 == s.tiles && tail) {
+                            // the partly filled last block was loaded to end its slot
+                            const int lo = s.len - tail - t0;
+                            const uint64_t low = (1ull << lo) - 1ull;
+                            vis_now = (vis_now & low) | ((vis_now & ~low) << (BS - tail));
+                        }
+                        const uint32_t vlo = (uint32_t)vis_now, vhi = (uint32_t)(vis_now >> 32);
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
                             x[c] = (((c < 32 ? vlo : vhi) >> (c & 31)) & 1u) ? x[c] : kNegInf;
@@ -808,6 +965,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const float m_new = resc ? mt : m_used;
                     alpha = resc ? ex2(m_used - m_new) : 1.f;
                     const float msub = m_new == kNegInf ? 0.f : m_new;
+                    // the row sum is taken over the rounded weights the MMA multiplies
                     const uint64_t se2 = f2(se, se), nm2 = f2(-msub, -msub);
                     uint64_t rsv[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -829,6 +987,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         break;
                     }
                     tc_fence_after();
+                    mend(t - 1);
                     if (__any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -849,55 +1008,9 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(Sh::kPFull + sb));
-                if (++vs == Sh::kVStages) {
-                    vs = 0;
-                    ++vround;
-                }
-                if (bad) {
-                    // rare: add the values taken out of V to the rows that see their keys
-                    ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)(J & 1), kWaitLimitNs);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (warp_on) {
-                        const int nblk = (s.len + BS - 1) / BS;
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + lane_base + c0, o);
-#pragma unroll 1
-                            for (int c = 0; c < kTreeKeys; ++c) {
-                                const int bi = t * BPT + c / BS;
-                                if (bi >= nblk)
-                                    break;
-                                const int shift = tail && bi == nblk - 1 ? BS - tail : 0;
-                                const int cell = c % BS - shift;
-                                if (cell < 0)
-                                    continue;
-                                int blk = __ldg(a.block_tables + (size_t)s.b * a.max_blocks + bi);
-                                blk = (unsigned)blk < (unsigned)a.num_blocks ? blk : 0;
-                                const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                                    a.value_cache + (((size_t)blk * BS + cell) * a.num_kv_heads + s.kvh) * D + c0);
-                                const bool see = real && ((vis >> c) & 1ull);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const uint32_t x = __ldg(v + i);
-                                    const uint32_t f = nonfinite2<BF16>(x);
-                                    const float2 y = unpack2<BF16>(x);
-                                    if (see && (f & 1u))
-                                        o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) + y.x);
-                                    if (see && (f >> 16))
-                                        o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) + y.y);
-                                }
-                            }
-                            tmem_st32(tO + lane_base + c0, o);
-                        }
-                        tmem_wait_st();
-                        tc_fence_before();
-                    }
-                }
+                vis = vis_now;
+                was_masked = masked;
+                scans += masked ? 1 : 0;
             }
             if (ok)
                 ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
@@ -905,6 +1018,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok || !warp_on)
                 continue;
             tc_fence_after();
+            mend(s.k1 - 1);
             if (s.k0 == 0 && s.k1 == s.tiles) {
                 // the whole item: output rows.  The four lanes of a quad trade
                 // 16-byte chunks, so that a store covers 64 bytes of a row.
@@ -947,7 +1061,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             } else {
                 // a part of an item: a record (m, l, O), part 1 if the item starts here
-                const size_t rec = (((size_t)blockIdx.x * 2 + w_share) * 2 + (s.k0 > 0 ? 0 : 1)) * kTreeRows + r;
+                const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (s.k0 > 0 ? 0 : 1)) * kTreeRows + r;
                 float4 *orec = reinterpret_cast<float4 *>(a.rec_o + rec * D);
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -1029,6 +1143,494 @@ tree_merge_kernel(const TreeArgs a)
         else
             *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
     }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: up to 32 per (sequence, kv head)
+// ---------------------------------------------------------------------------
+// Small trees (or few heads to a group) leave the 128-row tiles above mostly
+// empty, and their calls are bound by the cache's bytes alone.  Here a warp
+// keeps all rows of an item in its own registers and streams pages through a
+// ring of its own, as the decode kernel does: no hand-over between warps, many
+// independent streams per SM.
+//   S[rows x keys] = Q K^T      mma.sync m16n8k16, Q as A, K rows as B
+//   O[rows x D]   += P V        P straight from S's registers as A, V as B
+// P is split into a 16-bit high part and a 16-bit remainder, each multiplied
+// by V, so the weights keep about 16 bits more.  CTA (part, kv head, sequence)
+// takes part_tokens keys; an item of one part is written out, of several as
+// records that tree_rows_merge_kernel joins.
+struct TreeRowsArgs {
+    const uint16_t *query;           // [T, Hq, D]
+    const int32_t *query_start;      // [batch + 1]
+    const int32_t *tree_mask;        // [T, words]
+    const uint16_t *value_cache;
+    const int32_t *block_tables;     // [batch, max_blocks]
+    const int32_t *context_lens;     // [batch]
+    uint16_t *out;                   // [T, Hq, D]
+    float2 *rec_ml;                  // [T * Hq, num_parts]
+    float *rec_o;                    // [T * Hq, num_parts, D]
+    int num_tokens;
+    int max_query_len;
+    int words;
+    int max_blocks;
+    int num_heads;
+    int num_kv_heads;
+    int group;
+    int num_blocks;
+    int part_tokens;                 // a multiple of the block size
+    int num_parts;
+    float scale_log2;
+};
+
+template <int D, int BS, int MT, int NW, int S>
+struct TreeRowsShape {
+    static constexpr int kRows = MT * 16;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = BS * 128;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kStageBytes = 2 * kTileBytes;
+    static constexpr int kRingBytes = NW * S * kStageBytes;
+    static constexpr int kMergeBytes = NW * kRows * (D + 2) * 4;
+    static constexpr int kQStride = D * 2 + 16;              // bytes of a Q row: ldmatrix without bank conflicts
+    static constexpr int kQBytes = MT > 1 ? kRows * kQStride : 0;
+    static constexpr int kMain = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kSmemBytes = kMain + kQBytes + 1024;
+#ifndef PKV_TUNE_REGS1
+#define PKV_TUNE_REGS1 168
+#endif
+#ifndef PKV_TUNE_REGS2
+#define PKV_TUNE_REGS2 232
+#endif
+    static constexpr int kCtas = 65536 / ((MT == 1 ? PKV_TUNE_REGS1 : PKV_TUNE_REGS2) * NW * 32);
+};
+
+template <int D, int BS, bool BF16, int MT, int NW, int S>
+__global__ void __launch_bounds__(NW * 32, TreeRowsShape<D, BS, MT, NW, S>::kCtas)
+tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const TreeRowsArgs a)
+{
+    using Sh = TreeRowsShape<D, BS, MT, NW, S>;
+    constexpr int KS = D / 16, NT = BS / 8, DT = D / 8;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[NW * S];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sq = smem + Sh::kMain;
+    const int part = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.group;
+    if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            mbar_init(smem_addr(&bars[warp * S + s]), 1);
+    }
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    fence_mbar_init();
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // this warp's first 32 table entries do not wait for the length
+    const int blk0 = part * (a.part_tokens / BS);
+    const int32_t *trow = a.block_tables + (size_t)b * a.max_blocks + blk0 + warp;
+    int ids;
+    {
+        const int lb = warp + lane * NW;
+        ids = lb < a.part_tokens / BS && blk0 + lb < a.max_blocks ? __ldg(trow + (size_t)lane * NW) : 0;
+    }
+    TreeSeq s;
+    if (!tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &s)) {
+        if (threadIdx.x == 0 && part == 0 && kvh == 0)
+            raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
+        return;
+    }
+    const int rows = s.n * G;                     // <= kRows
+    const int tok0 = part * a.part_tokens;
+    const int tok1 = min(s.len, tok0 + a.part_tokens);
+    if (rows == 0 || tok1 <= tok0)
+        return;
+    const bool split = s.len > a.part_tokens;
+    const int base = s.len - s.n;
+    const int nblk = (tok1 - tok0 + BS - 1) / BS;
+    const int nk = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;   // this warp's blocks
+    uint8_t *ring = smem + (size_t)warp * S * Sh::kStageBytes;
+    const uint32_t ring_s = smem_addr(ring);
+    const uint32_t bar0 = smem_addr(&bars[warp * S]);
+    const uint64_t policy = policy_evict_first();
+    auto issue = [&](int k) {
+        if ((k & 31) == 0 && k > 0)
+            ids = k + lane < nk ? __ldg(trow + (size_t)(k + lane) * NW) : 0;
+        int blk = __shfl_sync(0xffffffffu, ids, k & 31);
+        if ((unsigned)blk >= (unsigned)a.num_blocks) {
+            if (lane == 0)
+                raise_flag(PKV_DEVFLAG_BLOCK_RANGE);
+            blk = 0;
+        }
+        if (lane == 0) {
+            const uint32_t bar = bar0 + 8u * (k % S);
+            const uint32_t dk = ring_s + (uint32_t)((k % S) * Sh::kStageBytes), dv = dk + Sh::kTileBytes;
+            mbar_arrive_expect_tx(bar, Sh::kStageBytes);
+#pragma unroll
+            for (int h = 0; h < Sh::kHalves; ++h) {
+                tma_load_3d(dk + h * Sh::kHalfBytes, &tm_k, bar, h * 64, kvh, blk * BS, policy);
+                tma_load_3d(dv + h * Sh::kHalfBytes, &tm_v, bar, h * 64, kvh, blk * BS, policy);
+            }
+        }
+    };
+    const int pre = nk < S ? nk : S;
+    for (int k = 0; k < pre; ++k)
+        issue(k);
+
+    // ---- Q: one 16-row tile in registers, two in shared memory ----
+    // row r is (node r / G, head r % G)
+    const int g0 = lane >> 2, c2 = (lane & 3) * 2;
+    auto q_row = [&](int r) {
+        return a.query + ((size_t)(s.q0 + r / G) * a.num_heads + (size_t)kvh * G + r % G) * D;
+    };
+    uint32_t qf[MT > 1 ? 1 : KS][4];
+    if constexpr (MT == 1) {
+        const uint32_t *q0 = reinterpret_cast<const uint32_t *>(q_row(g0 < rows ? g0 : 0) + c2);
+        const uint32_t *q1 = reinterpret_cast<const uint32_t *>(q_row(g0 + 8 < rows ? g0 + 8 : 0) + c2);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            qf[ks][0] = __ldg(q0 + ks * 8);
+            qf[ks][1] = __ldg(q1 + ks * 8);
+            qf[ks][2] = __ldg(q0 + ks * 8 + 4);
+            qf[ks][3] = __ldg(q1 + ks * 8 + 4);
+        }
+    } else {
+        for (int i = threadIdx.x; i < Sh::kRows * (D / 8); i += NW * 32) {
+            const int r = i / (D / 8), v = i % (D / 8);
+            *reinterpret_cast<uint4 *>(sq + r * Sh::kQStride + v * 16) =
+                r < rows ? __ldg(reinterpret_cast<const uint4 *>(q_row(r)) + v) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncthreads();
+    }
+    const uint32_t sq_s = smem_addr(sq) + (uint32_t)((lane & 15) * Sh::kQStride + (lane >> 4) * 16);
+    // this lane's rows' nodes, for their mask rows
+    int node[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = mt * 16 + h * 8 + g0;
+            node[mt][h] = r < rows ? r / G : 0;
+        }
+
+    float m_run[MT][2], l_run[MT][2], acc[MT][DT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m_run[mt][0] = m_run[mt][1] = kNegInf;
+        l_run[mt][0] = l_run[mt][1] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[mt][d][i] = 0.f;
+    }
+    int issued = pre, consumed = 0;
+    for (int k = 0; k < nk; ++k) {
+        const int st = k % S;
+        const bool got = mbar_wait_bounded(bar0 + 8u * st, (uint32_t)((k / S) & 1), kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, got)) {
+            if (lane == 0)
+                raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+            break;
+        }
+        consumed = k + 1;
+        const uint32_t sk = ring_s + (uint32_t)(st * Sh::kStageBytes), sv = sk + Sh::kTileBytes;
+        const int p0 = (blk0 + warp + k * NW) * BS;      // the block's first position
+        const bool masked = p0 + BS > base;
+        bool bad = false;
+        if (masked) {
+            // cells past the end may hold anything: zero; infinities and NaN
+            // of drafted cells are zeroed too and added below to the rows that
+            // see them (weight 0 times such a value would not be 0)
+            uint8_t *vt = ring + (size_t)st * Sh::kStageBytes + Sh::kTileBytes;
+            const int valid = min(BS, s.len - p0);
+            uint32_t any = 0u;
+#pragma unroll
+            for (int i = 0; i < Sh::kTileBytes / 512; ++i) {
+                const int v = i * 32 + lane;
+                const int row = (v >> 3) % BS;
+                uint4 *at = reinterpret_cast<uint4 *>(vt) + v;
+                const uint4 x = *at;
+                if (row >= valid)
+                    *at = make_uint4(0u, 0u, 0u, 0u);
+                else
+                    any |= nonfinite2<BF16>(x.x) | nonfinite2<BF16>(x.y) | nonfinite2<BF16>(x.z) | nonfinite2<BF16>(x.w);
+            }
+            bad = __any_sync(0xffffffffu, any != 0u);
+            if (bad) {
+#pragma unroll 1
+                for (int i = 0; i < Sh::kTileBytes / 4 / 32; ++i) {
+                    uint32_t *at = reinterpret_cast<uint32_t *>(vt) + i * 32 + lane;
+                    *at &= ~(nonfinite2<BF16>(*at) * 0xffffu);
+                }
+            }
+            // order these generic stores before any later TMA (async proxy) write
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        }
+        // ---- scores ----
+        float sc[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc[mt][j][i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t qa[MT][4];
+            if constexpr (MT == 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    qa[0][i] = qf[ks][i];
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    ldsm_x4(sq_s + (uint32_t)(mt * 16 * Sh::kQStride + ks * 32), qa[mt]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+                const int key = j * 8 + (lane >> 4) * 8 + (lane & 7);
+                const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
+                uint32_t kf[4];
+                ldsm_x4(sk + (uint32_t)((ks >> 2) * Sh::kHalfBytes + key * 128 + ((chunk ^ (key & 7)) << 4)), kf);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma_16816<BF16>(sc[mt][j], qa[mt], kf[0], kf[1]);
+                    mma_16816<BF16>(sc[mt][j + 1], qa[mt], kf[2], kf[3]);
+                }
+            }
+        }
+        // ---- mask, online softmax (base 2) ----
+        uint32_t vis[MT][2];
+        bool any_resc = false;
+        float alpha[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                vis[mt][h] = 0xffffffffu;
+                if (masked) {
+                    const int32_t *mrow = a.tree_mask + (size_t)(s.q0 + node[mt][h]) * a.words;
+                    const uint32_t mw[3] = {(uint32_t)__ldg(mrow), a.words > 1 ? (uint32_t)__ldg(mrow + 1) : 0u, 0u};
+                    vis[mt][h] = (uint32_t)tree_bits(mrow, mw, a.words, base, s.n, p0);
+                }
+                float mx = kNegInf;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &x = sc[mt][j][2 * h + i];
+                        x *= a.scale_log2;
+                        if (masked)
+                            x = (vis[mt][h] >> (j * 8 + c2 + i)) & 1u ? x : kNegInf;
+                        mx = fmaxf(mx, x);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // the running maximum moves when a block exceeds it by 2^8
+                const bool move = mx > m_run[mt][h] + 8.f;
+                const float mnew = move ? mx : m_run[mt][h];
+                alpha[mt][h] = move ? ex2(m_run[mt][h] - mnew) : 1.f;
+                any_resc |= move;
+                m_run[mt][h] = mnew;
+                const float msub = mnew == kNegInf ? 0.f : mnew;
+                float ls = 0.f;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &x = sc[mt][j][2 * h + i];
+                        x = ex2(x - msub);
+                        ls += x;
+                    }
+                l_run[mt][h] = l_run[mt][h] * alpha[mt][h] + ls;
+            }
+        }
+        if (__any_sync(0xffffffffu, any_resc)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    acc[mt][d][0] *= alpha[mt][0];
+                    acc[mt][d][1] *= alpha[mt][0];
+                    acc[mt][d][2] *= alpha[mt][1];
+                    acc[mt][d][3] *= alpha[mt][1];
+                }
+        }
+        // ---- O += P V, 16 keys at a time ----
+#pragma unroll
+        for (int kb = 0; kb < BS / 16; ++kb) {
+            uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float *x = &sc[mt][2 * kb + (i >> 1)][2 * (i & 1)];
+                    ph[mt][i] = pack2<BF16>(x[0], x[1]);
+                    const float2 f = unpack2<BF16>(ph[mt][i]);
+                    pl[mt][i] = pack2<BF16>(x[0] - f.x, x[1] - f.y);
+                }
+            const int key = kb * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int d = 0; d < DT; d += 2) {
+                const int chunk = (d & 7) + (lane >> 4);
+                uint32_t vf[4];
+                ldsm_x4_trans(sv + (uint32_t)((d >> 3) * Sh::kHalfBytes + key * 128 + ((chunk ^ (key & 7)) << 4)), vf);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma_16816<BF16>(acc[mt][d], ph[mt], vf[0], vf[1]);
+                    mma_16816<BF16>(acc[mt][d + 1], ph[mt], vf[2], vf[3]);
+                    mma_16816<BF16>(acc[mt][d], pl[mt], vf[0], vf[1]);
+                    mma_16816<BF16>(acc[mt][d + 1], pl[mt], vf[2], vf[3]);
+                }
+            }
+        }
+        if (bad) {
+            int blk = __ldg(a.block_tables + (size_t)b * a.max_blocks + p0 / BS);
+            blk = (unsigned)blk < (unsigned)a.num_blocks ? blk : 0;
+#pragma unroll 1
+            for (int c = 0; c < min(BS, s.len - p0); ++c) {
+                const uint32_t *v = reinterpret_cast<const uint32_t *>(
+                    a.value_cache + (((size_t)blk * BS + c) * a.num_kv_heads + kvh) * D + c2);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const uint32_t x = __ldg(v + d * 4);
+                    const uint32_t f = nonfinite2<BF16>(x);
+                    const float2 y = unpack2<BF16>(x);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if ((vis[mt][h] >> c) & 1u) {
+                                if (f & 1u)
+                                    acc[mt][d][2 * h] += y.x;
+                                if (f >> 16)
+                                    acc[mt][d][2 * h + 1] += y.y;
+                            }
+                }
+            }
+        }
+        __syncwarp();
+        if (k + S < nk) {
+            issue(k + S);
+            issued = k + S + 1;
+        }
+    }
+    // a wait gave up: copies in flight land (bounded) before the memory is reused
+    for (int k = consumed; k < issued; ++k)
+        mbar_wait_bounded(bar0 + 8u * (k % S), (uint32_t)((k / S) & 1), kWaitLimitNs / 8);
+
+    // ---- merge the warps by log-sum-exp through shared memory ----
+    __syncthreads();
+    float *so = reinterpret_cast<float *>(smem);         // [NW][kRows][D]
+    float2 *sml = reinterpret_cast<float2 *>(so + NW * Sh::kRows * D);   // [NW][kRows]
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = mt * 16 + h * 8 + g0;
+            float l = l_run[mt][h];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if ((lane & 3) == 0)
+                sml[warp * Sh::kRows + r] = make_float2(m_run[mt][h], l);
+            if (r < rows) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    *reinterpret_cast<float2 *>(so + (warp * Sh::kRows + r) * D + d * 8 + c2) =
+                        make_float2(acc[mt][d][2 * h], acc[mt][d][2 * h + 1]);
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += NW * 32) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        float M = kNegInf;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            M = fmaxf(M, sml[w * Sh::kRows + r].x);
+        float den = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float2 ml = sml[w * Sh::kRows + r];
+            const float e = ml.x == kNegInf ? 1.f : ex2(ml.x - M);   // (1: no keys seen, or all NaN)
+            const float4 o = *reinterpret_cast<const float4 *>(so + (w * Sh::kRows + r) * D + d);
+            den += e * ml.y;
+            num.x += e * o.x;
+            num.y += e * o.y;
+            num.z += e * o.z;
+            num.w += e * o.w;
+        }
+        const size_t row = (size_t)(s.q0 + r / G) * a.num_heads + (size_t)kvh * G + r % G;
+        if (!split) {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            *reinterpret_cast<uint2 *>(a.out + row * D + d) =
+                make_uint2(pack2<BF16>(num.x * inv, num.y * inv), pack2<BF16>(num.z * inv, num.w * inv));
+        } else {
+            const size_t rec = row * a.num_parts + part;
+            *reinterpret_cast<float4 *>(a.rec_o + rec * D + d) = num;
+            if (d == 0)
+                a.rec_ml[rec] = make_float2(M, den);
+        }
+    }
+}
+
+// Records of the items of several parts, a warp per row: grid (eights of the
+// rows, kv heads, sequences).
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256)
+tree_rows_merge_kernel(const TreeRowsArgs a, int block_size)
+{
+    constexpr int V = D / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TreeSeq s;
+    if (!tree_seq(a.query_start, a.context_lens, blockIdx.z, a.num_tokens, a.max_query_len,
+                  a.max_blocks * block_size, &s))
+        return;
+    const int r = blockIdx.x * 8 + warp;
+    const int np = (s.len + a.part_tokens - 1) / a.part_tokens;
+    if (np <= 1 || r >= s.n * a.group)
+        return;
+    const size_t row = (size_t)(s.q0 + r / a.group) * a.num_heads + (size_t)blockIdx.y * a.group + r % a.group;
+    const float2 *ml = a.rec_ml + row * a.num_parts;
+    float M = kNegInf;
+    for (int k = lane; k < np; k += 32)
+        M = fmaxf(M, __ldg(&ml[k].x));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float den = 0.f, acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        acc[i] = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < np; ++k) {
+        const float2 x = __ldg(ml + k);
+        float v[V];
+        load_slice<D>(a.rec_o + (row * a.num_parts + k) * D + lane * V, v);
+        const float f = x.x == kNegInf ? 1.f : ex2(x.x - M);         // (1: no keys seen, or all NaN)
+        den += f * x.y;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[i] += f * v[i];
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    uint16_t *o = a.out + row * D + lane * V;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),
+                                                   pack2<BF16>(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
 }
 
 }  // namespace pkv

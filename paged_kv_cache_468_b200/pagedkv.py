@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
         L.pkv_draft_tree_accept.restype = i32
         L.pkv_draft_tree_accept.argtypes = [P, P, P, i32, P, i32, i32, P, P, P, P]
         L.pkv_tree_workspace_bytes.restype = sz
-        L.pkv_tree_workspace_bytes.argtypes = [i32] * 7
+        L.pkv_tree_workspace_bytes.argtypes = [i32] * 8
         L.pkv_paged_attention_tree.restype = i32
         L.pkv_paged_attention_tree.argtypes = [P, i32, P, i32, P, P, P, P, i32, P, i32, i32, i32, i32,
                                                i32, i64, f32, P, sz, P, i32, P]
@@ -489,10 +489,10 @@ def draft_tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, p
     return path, lens, following
 
 
-def tree_workspace_bytes(batch: int, max_query_len: int, num_heads: int, num_kv_heads: int, head_dim: int,
-                         max_blocks: int, block_size: int) -> int:
-    return int(lib().pkv_tree_workspace_bytes(batch, max_query_len, num_heads, num_kv_heads, head_dim,
-                                              max_blocks, block_size))
+def tree_workspace_bytes(batch: int, max_query_len: int, num_tokens: int, num_heads: int, num_kv_heads: int,
+                         head_dim: int, max_blocks: int, block_size: int) -> int:
+    return int(lib().pkv_tree_workspace_bytes(batch, max_query_len, num_tokens, num_heads, num_kv_heads,
+                                              head_dim, max_blocks, block_size))
 
 
 def paged_attention_tree(query: torch.Tensor, query_start: torch.Tensor, max_query_len: int,
@@ -530,7 +530,7 @@ def paged_attention_tree(query: torch.Tensor, query_start: torch.Tensor, max_que
         out = _empty((T, Hq, D), query.dtype, dev, stream)
     out_ptr = _tensor(out, "out", query.dtype, (T, Hq, D), dev)
     ws_ptr, ws_bytes, workspace = _scratch(
-        workspace, tree_workspace_bytes(B, int(max_query_len), Hq, Hkv, D, MB, bs), dev, stream)
+        workspace, tree_workspace_bytes(B, int(max_query_len), T, Hq, Hkv, D, MB, bs), dev, stream)
     with _on_device(dev):
         st = lib().pkv_paged_attention_tree(*head, ws_ptr, ws_bytes, out_ptr, dt, _stream_handle(stream, dev))
     _check(st, "pkv_paged_attention_tree")

@@ -64,7 +64,8 @@ def test_tree_attention_host_validation():
     assert call(mask=A16 + 2) == pagedkv.ERR_MISALIGNED
     assert call(B=0, q=None, out=None) == pagedkv.OK
     assert call(T=0, q=None, out=None) == pagedkv.OK
-    need = pkv.tree_workspace_bytes(2, 32, 8, 2, 128, 8, 16)
+    need = pkv.tree_workspace_bytes(2, 32, 64, 8, 2, 128, 8, 16)
+    assert need > 0
     if need:
         assert call(ws=None) == pagedkv.ERR_WORKSPACE
         assert call(wsb=need - 1) == pagedkv.ERR_WORKSPACE
