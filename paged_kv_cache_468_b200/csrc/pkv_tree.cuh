@@ -381,6 +381,17 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x)   // bit 0: low half,
     return ((y & 0xffffu) == (e & 0xffffu) ? 1u : 0u) | ((y >> 16) == (e >> 16) ? 0x10000u : 0u);
 }
 
+// acc stays 0 until a value is an infinity or a NaN (0 times it is NaN).
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma_zero2(uint32_t x, uint32_t acc)
+{
+    if constexpr (BF16)
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
+}
+
 // O_row += the infinities and NaN of V's rows of key tile t that the row sees
 // (they were zeroed in shared memory).  Rare, so simple: one key at a time,
 // read from the cache again.
@@ -743,13 +754,17 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         break;
                     }
                     uint4 *vt = reinterpret_cast<uint4 *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
-                    uint32_t any = 0u;
+                    uint32_t any[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 8
                     for (int i = 0; i < Sh::kKVBytes / 512; ++i) {
                         const uint4 x = vt[i * 32];
-                        any |= nonfinite2<BF16>(x.x) | nonfinite2<BF16>(x.y) | nonfinite2<BF16>(x.z) | nonfinite2<BF16>(x.w);
+                        any[0] = fma_zero2<BF16>(x.x, any[0]);
+                        any[1] = fma_zero2<BF16>(x.y, any[1]);
+                        any[2] = fma_zero2<BF16>(x.z, any[2]);
+                        any[3] = fma_zero2<BF16>(x.w, any[3]);
                     }
-                    const bool bad = __any_sync(0xffffffffu, any != 0u);
+                    // (a sum of zeros is 0 or -0)
+                    const bool bad = __any_sync(0xffffffffu, ((any[0] | any[1] | any[2] | any[3]) & 0x7fff7fffu) != 0u);
                     if (bad) {
                         uint32_t *w = reinterpret_cast<uint32_t *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
 #pragma unroll 1
@@ -883,20 +898,15 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ---- softmax and epilogue: thread = row r of the tile = TMEM lane r ----
         const int r = warp * 32 + lane;
         const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const int q = lane & 3;
         const int r_tok = r / G, r_head = r - r_tok * G;
-        int rq_tok = r_tok, rq_head = r_head - q;    // the first row of this lane's quad
-        while (rq_head < 0) {
-            rq_head += G;
-            --rq_tok;
-        }
         const float sc = a.scale_log2;
         const bool fold = sc > 0.f;                  // a positive scale joins the exponent's fma
         const float sm = fold ? 1.f : sc, se = fold ? sc : 1.f;
         bool ok = true;
         int J = 0, scans = 0;
         TreePart s;
-        while (ok && next_part(&s, false)) {
+        bool has = next_part(&s, false);
+        while (ok && has) {
             const int rows = min(R, s.n * G - s.rt * R);      // rows of this tile
             const bool warp_on = warp * 32 < rows;
             const bool real = r < rows;
@@ -1012,71 +1022,56 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 was_masked = masked;
                 scans += masked ? 1 : 0;
             }
-            if (ok)
-                ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
+            if (!ok)
+                break;
+            TreePart nx;                             // read while the last P V runs
+            has = next_part(&nx, false);
+            const size_t orow = (size_t)(s.q0 + s.rt * TT + r_tok) * a.num_heads + (size_t)s.kvh * G + r_head;
+            const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+            ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok || !warp_on)
-                continue;
-            tc_fence_after();
-            mend(s.k1 - 1);
-            if (s.k0 == 0 && s.k1 == s.tiles) {
-                // the whole item: output rows.  The four lanes of a quad trade
-                // 16-byte chunks, so that a store covers 64 bytes of a row.
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint4 *orow[4];
-                int tk = rq_tok, hd = rq_head;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    orow[h] = r - q + h < rows
-                                  ? reinterpret_cast<uint4 *>(a.out + ((size_t)(s.q0 + s.rt * TT + tk) * a.num_heads +
-                                                                       (size_t)s.kvh * G + hd) * D)
-                                  : nullptr;
-                    if (++hd == G) {
-                        hd = 0;
-                        ++tk;
-                    }
-                }
+            if (ok && warp_on) {
+                tc_fence_after();
+                mend(s.k1 - 1);
+                if (s.k0 == 0 && s.k1 == s.tiles) {
+                    // the whole item: output rows
+                    uint4 *o16 = reinterpret_cast<uint4 *>(a.out + orow * D);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t o[64];
-                    tmem_ld64(tO + lane_base + c0, o);
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        uint32_t o[64];
+                        tmem_ld64(tO + lane_base + c0, o);
+                        if (real) {
 #pragma unroll
-                    for (int g2 = 0; g2 < 2; ++g2) {
-                        uint4 ch[4];
+                            for (int v = 0; v < 8; ++v) {
+                                uint32_t w[4];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack2<BF16>(__uint_as_float(o[32 * g2 + 8 * v + 2 * e]) * inv,
-                                                   __uint_as_float(o[32 * g2 + 8 * v + 2 * e + 1]) * inv);
-                            ch[v] = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = pack2<BF16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                                       __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+                                o16[c0 / 8 + v] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
                         }
-                        quad_transpose(ch, q);
-#pragma unroll
-                        for (int h = 0; h < 4; ++h)
-                            if (orow[h] != nullptr)
-                                orow[h][(c0 + 32 * g2) / 8 + q] = ch[h];
                     }
-                }
-            } else {
-                // a part of an item: a record (m, l, O), part 1 if the item starts here
-                const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (s.k0 > 0 ? 0 : 1)) * kTreeRows + r;
-                float4 *orec = reinterpret_cast<float4 *>(a.rec_o + rec * D);
+                } else {
+                    // a part of an item: a record (m, l, O), part 1 if the item starts here
+                    const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (s.k0 > 0 ? 0 : 1)) * kTreeRows + r;
+                    float4 *orec = reinterpret_cast<float4 *>(a.rec_o + rec * D);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + lane_base + c0, o);
-                    if (real) {
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + lane_base + c0, o);
+                        if (real) {
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            orec[c0 / 4 + v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                                           __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                            for (int v = 0; v < 8; ++v)
+                                orec[c0 / 4 + v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                                               __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                        }
                     }
+                    if (real)
+                        a.rec_ml[rec] = make_float2(m_used, l);
                 }
-                if (real)
-                    a.rec_ml[rec] = make_float2(m_used, l);
             }
+            s = nx;
             // the next part's first P V overwrites O after this warp's next P
         }
         if (!ok && lane == 0)
@@ -1360,9 +1355,9 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (row >= valid)
                     *at = make_uint4(0u, 0u, 0u, 0u);
                 else
-                    any |= nonfinite2<BF16>(x.x) | nonfinite2<BF16>(x.y) | nonfinite2<BF16>(x.z) | nonfinite2<BF16>(x.w);
+                    any = fma_zero2<BF16>(x.x, fma_zero2<BF16>(x.y, fma_zero2<BF16>(x.z, fma_zero2<BF16>(x.w, any))));
             }
-            bad = __any_sync(0xffffffffu, any != 0u);
+            bad = __any_sync(0xffffffffu, (any & 0x7fff7fffu) != 0u);
             if (bad) {
 #pragma unroll 1
                 for (int i = 0; i < Sh::kTileBytes / 4 / 32; ++i) {
