@@ -1199,10 +1199,14 @@ extern "C" pkv_status pkv_draft_tree_accept(const int64_t *draft_tokens, const i
         return fail(PKV_ERR_MISALIGNED, "draft_tokens/target_tokens/next_tokens must be 8-byte aligned");
     if (!aligned4(parents) || !aligned4(query_start) || !aligned4(accept_path) || !aligned4(accept_lens))
         return fail(PKV_ERR_MISALIGNED, "parents/query_start/accept_path/accept_lens must be 4-byte aligned");
-    const cudaError_t e = launch_pdl(pkv::tree_accept_kernel, dim3((unsigned)batch), dim3(pkv::kAcceptThreads), 0,
-                                     static_cast<cudaStream_t>(stream), draft_tokens, target_tokens, parents,
-                                     num_tokens, query_start, max_query_len, accept_path, accept_lens,
-                                     next_tokens);
+    auto go = [&](auto kern, unsigned threads) {
+        return launch_pdl(kern, dim3((unsigned)batch), dim3(threads), 0, static_cast<cudaStream_t>(stream),
+                          draft_tokens, target_tokens, parents, num_tokens, query_start, max_query_len,
+                          accept_path, accept_lens, next_tokens);
+    };
+    // a thread to a node for usual trees, two for the widest
+    const cudaError_t e = max_query_len <= 64 ? go(pkv::tree_accept_kernel<64>, 64)
+                                              : go(pkv::tree_accept_kernel<512>, 512);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_accept_kernel launch");
     return PKV_OK;
@@ -1218,7 +1222,7 @@ struct TreePlan {
     size_t ml, o, total;        // workspace offsets (128-row tiles: the descriptors come first)
 };
 #ifndef PKV_TUNE_FEW
-#define PKV_TUNE_FEW 32
+#define PKV_TUNE_FEW 16
 #endif
 #ifndef PKV_TUNE_PARTS
 #define PKV_TUNE_PARTS 592
@@ -1489,11 +1493,48 @@ extern "C" pkv_status pkv_paged_attention_tree(
 // ---------------------------------------------------------------------------
 // Compaction of kept cells
 // ---------------------------------------------------------------------------
+namespace {
+
+// Slices and chunks of a compaction call.  Lists of up to 256 entries are one
+// chunk each, of slices that are narrow enough: two vectors to a thread up to
+// 16 entries (accepted paths: 16 sequences x 16 layers x 3 cells take 2.9 us
+// so, 4.3 with eight), eight beyond (31 x 16 x up to 54 cells: 7.0 us so, 9.2
+// with two; 34 sequences of up to 200 entries: 6 us, as long lists 14 us).  Longer ones take slices of up to 2 KB (a whole cell of
+// 8 heads of 128), which DRAM pages like best.
+struct CompactPlan {
+    int vec;                    // vectors per thread of the short kernel, 0: the long one
+    int slice_vec, slices, rows;
+    int64_t chunks;             // of the longest list
+};
+CompactPlan compact_plan(int max_keep, int num_kv_heads, int head_dim)
+{
+    CompactPlan p;
+    const int vec = num_kv_heads * head_dim / 8;
+    p.vec = max_keep <= 16 ? 2 : (max_keep <= pkv::kCompactThreads ? 8 : 0);
+    const int chunk_vec = p.vec ? pkv::kCompactThreads * p.vec : pkv::kCompactStage / 16;
+    const int most = p.vec ? std::min(128, chunk_vec / std::max(1, max_keep)) : 128;
+    p.slices = (vec + most - 1) / most;
+    p.slice_vec = (vec + p.slices - 1) / p.slices;
+    p.rows = p.vec ? chunk_vec / p.slice_vec : std::min(32, chunk_vec / p.slice_vec);
+    p.chunks = p.vec ? 1 : ((int64_t)max_keep + p.rows - 1) / p.rows;
+    return p;
+}
+
+// Flags of a call: the counter and one per (chunk, sequence, cache, slice) of a launch's layers.
+int64_t compact_flags(const CompactPlan &p, int num_layers, int batch)
+{
+    return p.vec ? 0 : 1 + p.chunks * batch * 2 * std::min(num_layers, pkv::kCompactMaxLayers) * p.slices;
+}
+
+}  // namespace
+
 extern "C" size_t pkv_compact_workspace_bytes(int num_layers, int batch, int max_keep, int num_kv_heads,
                                               int head_dim)
 {
-    (void)num_layers, (void)batch, (void)max_keep, (void)num_kv_heads, (void)head_dim;
-    return 0;
+    if (num_layers <= 0 || batch <= 0 || max_keep <= 0 || num_kv_heads <= 0 || head_dim <= 0 || head_dim % 8 != 0 ||
+        (int64_t)num_kv_heads * head_dim > (int64_t)1 << 24)
+        return 0;
+    return (size_t)compact_flags(compact_plan(max_keep, num_kv_heads, head_dim), num_layers, batch) * sizeof(unsigned int);
 }
 
 extern "C" pkv_status pkv_kv_cache_compact(void *const *key_caches, void *const *value_caches,
@@ -1544,6 +1585,24 @@ extern "C" pkv_status pkv_kv_cache_compact(void *const *key_caches, void *const 
     a.block_size = block_size;
     a.num_blocks = (int)num_blocks;
     a.vec_per_cell = num_kv_heads * head_dim / 8;
+    const CompactPlan plan = compact_plan(max_keep, num_kv_heads, head_dim);
+    const int64_t flags = compact_flags(plan, num_layers, batch);
+    const int64_t columns = (int64_t)batch * 2 * std::min(num_layers, pkv::kCompactMaxLayers) * plan.slices;
+    if (flags >= (int64_t)1 << 31 || columns >= (int64_t)1 << 31)
+        return fail(PKV_ERR_UNSUPPORTED, "batch x layers x chunks of max_keep is 2^31 or more");
+    if (flags > 0) {
+        if (!workspace || workspace_bytes < (size_t)flags * sizeof(unsigned int))
+            return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given",
+                        (size_t)flags * sizeof(unsigned int), workspace ? workspace_bytes : (size_t)0);
+        if (!aligned4(workspace))
+            return fail(PKV_ERR_MISALIGNED, "workspace must be 4-byte aligned");
+    }
+    a.batch = batch;
+    a.flags = static_cast<unsigned int *>(workspace);
+    a.slice_vec = plan.slice_vec;
+    a.slices = plan.slices;
+    a.rows = plan.rows;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int l0 = 0; l0 < num_layers; l0 += pkv::kCompactMaxLayers) {
         const int layers = std::min(num_layers - l0, pkv::kCompactMaxLayers);
         for (int i = 0; i < 2 * pkv::kCompactMaxLayers; ++i)
@@ -1552,10 +1611,20 @@ extern "C" pkv_status pkv_kv_cache_compact(void *const *key_caches, void *const 
             a.cache[i] = static_cast<uint4 *>(key_caches[l0 + i]);
             a.cache[layers + i] = static_cast<uint4 *>(value_caches[l0 + i]);
         }
-        const dim3 grid((unsigned)((a.vec_per_cell + pkv::kCompactThreads - 1) / pkv::kCompactThreads),
-                        (unsigned)(2 * layers), (unsigned)batch);
-        const cudaError_t e = launch_pdl(pkv::compact_kernel, grid, dim3(pkv::kCompactThreads), 0,
-                                         static_cast<cudaStream_t>(stream), a);
+        a.caches = 2 * layers;
+        const int64_t cols = (int64_t)batch * a.caches * a.slices;
+        cudaError_t e;
+        if (flags > 0) {
+            if ((e = cudaMemsetAsync(workspace, 0, (size_t)(1 + plan.chunks * cols) * sizeof(unsigned int), st)) != cudaSuccess)
+                return cuda_fail(e, "cudaMemsetAsync(compaction flags)");
+            // as many one-warp CTAs as an SM's shared memory holds; they take chunk after chunk
+            static_assert(pkv::kCompactPerSm * (pkv::kCompactStage + 16 + 1024) <= 228 * 1024, "CTAs per SM");
+            const int64_t ctas = std::min<int64_t>(plan.chunks * cols, pkv::kCompactPerSm * kPlanSmCount);
+            e = launch_pdl(pkv::compact_long_kernel, dim3((unsigned)ctas), dim3(32), pkv::kCompactStage, st, a);
+        } else {
+            e = launch_pdl(plan.vec == 2 ? pkv::compact_short_kernel<2> : pkv::compact_short_kernel<8>,
+                           dim3((unsigned)cols), dim3(pkv::kCompactThreads), 0, st, a);
+        }
         if (e != cudaSuccess)
             return cuda_fail(e, "compact_kernel launch");
     }

@@ -117,8 +117,18 @@ tree_mask_kernel(const int32_t *__restrict__ parents, int num_tokens, const int3
         positions[s.q0 + i0 + lane] = s.len - s.n + depth;
     // rows of `words` words are contiguous: lane after lane over the warp's rows
     int32_t *out = tree_mask + (size_t)(s.q0 + i0) * words;
-    for (int e = lane; e < rows * words; e += 32)
-        out[e] = (int32_t)s_row[warp][e / words][e % words];
+    const int r_step = 32 / words, w_step = 32 - r_step * words;
+    int r = lane / words, w = lane - r * words;
+#pragma unroll 4
+    for (int e = lane; e < rows * words; e += 32) {
+        out[e] = (int32_t)s_row[warp][r][w];
+        r += r_step;
+        w += w_step;
+        if (w >= words) {
+            w -= words;
+            ++r;
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -130,8 +140,8 @@ tree_mask_kernel(const int32_t *__restrict__ parents, int num_tokens, const int3
 // shared memory: the result does not depend on the order), one thread follows
 // the winners.  A CTA per sequence; bound by launch and two round trips to
 // memory.
-constexpr int kAcceptThreads = 128;
-__global__ void __launch_bounds__(kAcceptThreads)
+template <int NT>
+__global__ void __launch_bounds__(NT)
 tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict__ target,
                    const int32_t *__restrict__ parents, int num_tokens,
                    const int32_t *__restrict__ query_start, int max_query_len,
@@ -146,10 +156,10 @@ tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict_
     TreeSeq s;
     if (!tree_seq(query_start, nullptr, b, num_tokens, max_query_len, 0, &s) && threadIdx.x == 0)
         raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);    // s.n is 0: an empty path
-    for (int i = threadIdx.x; i < s.n; i += kAcceptThreads)
+    for (int i = threadIdx.x; i < s.n; i += NT)
         s_next[i] = kTreeMaxNodes;
     __syncthreads();
-    for (int i = threadIdx.x; i < s.n; i += kAcceptThreads) {
+    for (int i = threadIdx.x; i < s.n; i += NT) {
         const int p = __ldg(parents + s.q0 + i);
         if (p < -1 || p >= i)
             raise_flag(PKV_DEVFLAG_INDEX_RANGE);   // never accepted
@@ -169,7 +179,7 @@ tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict_
     }
     __syncthreads();
     const int k = s_len;
-    for (int i = threadIdx.x; i < max_query_len; i += kAcceptThreads)
+    for (int i = threadIdx.x; i < max_query_len; i += NT)
         path[(size_t)b * max_query_len + i] = i < k ? (int)s_path[i] : -1;
 }
 

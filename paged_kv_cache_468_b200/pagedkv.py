@@ -39,6 +39,8 @@ class PagedKVError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (raises RuntimeError if it is not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -404,37 +406,57 @@ def paged_attention_decode_cascade(query: torch.Tensor, key_cache: torch.Tensor,
 
 
 # ---- speculative decoding with drafted token trees ----
+# These calls run many times per generated token, so the checks below are kept
+# to a few attribute reads per tensor.
 def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
     """Address of a dense CUDA tensor of this type and shape on `device`."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')} {list(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return _dev(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _cuda_device(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _empty(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     """A new tensor whose memory the caching allocator reuses in `stream`'s order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(workspace: Optional[torch.Tensor], need: int, device, stream) -> tuple:
+def _scratch(like: torch.Tensor, workspace: Optional[torch.Tensor], need: int, stream) -> tuple:
     """(address, bytes, tensor to keep alive) of a workspace of `need` bytes."""
     if not need:
         return None, 0, None
     if workspace is None:
-        workspace = _empty(need, torch.uint8, device, stream)
-    elif workspace.device != device:
-        raise ValueError(f"workspace must be on {device}")
+        workspace = _empty(like, (need,), torch.uint8, stream)
+    elif workspace.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
     return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
 
 
-def _on_device(device: torch.device):
-    """The device made current for a launch (the stream belongs to it)."""
-    return torch.cuda.device(device)
+def _launch(call, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> int:
+    """call(*args, stream handle) with `device` current (the stream belongs to it)."""
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"the stream must be one of {device}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        return call(*args, handle)
+    with torch.cuda.device(index):
+        return call(*args, handle)
 
 
 def _tree_rows(query_start: torch.Tensor, max_query_len: int) -> int:
@@ -452,16 +474,14 @@ def draft_tree_mask(parents: torch.Tensor, query_start: torch.Tensor, max_query_
     context_lens int32 [B] (the drafted tokens included) -> tree_mask int32 [T, ceil(max_query_len / 32)],
     positions int32 [T].  Rows of T outside every sequence are not written."""
     B = _tree_rows(query_start, max_query_len)
-    dev = parents.device
+    dev = _cuda_device(parents, "parents")
     T, W = parents.shape[0] if parents.dim() == 1 else -1, -(-int(max_query_len) // 32)
     args = (_tensor(parents, "parents", torch.int32, (T,), dev), T,
             _tensor(query_start, "query_start", torch.int32, (B + 1,), dev), int(max_query_len),
             _tensor(context_lens, "context_lens", torch.int32, (B,), dev), B)
-    mask = _empty((T, W), torch.int32, dev, stream)
-    positions = _empty((T,), torch.int32, dev, stream)
-    with _on_device(dev):
-        st = lib().pkv_draft_tree_mask(*args, _dev(mask, "tree_mask"), _dev(positions, "positions"),
-                                       _stream_handle(stream, dev))
+    mask = _empty(parents, (T, W), torch.int32, stream)
+    positions = _empty(parents, (T,), torch.int32, stream)
+    st = _launch(lib().pkv_draft_tree_mask, dev, stream, *args, mask.data_ptr(), positions.data_ptr())
     _check(st, "pkv_draft_tree_mask")
     return mask, positions
 
@@ -473,18 +493,16 @@ def draft_tree_accept(draft_tokens: torch.Tensor, target_tokens: torch.Tensor, p
     int64 [T], parents int32 [T], query_start int32 [B+1] -> accept_path int32 [B, max_query_len]
     (accepted nodes, then -1), accept_lens int32 [B], next_tokens int64 [B]."""
     B = _tree_rows(query_start, max_query_len)
-    dev = parents.device
+    dev = _cuda_device(parents, "parents")
     T = parents.shape[0] if parents.dim() == 1 else -1
     args = (_tensor(draft_tokens, "draft_tokens", torch.int64, (T,), dev),
             _tensor(target_tokens, "target_tokens", torch.int64, (T,), dev),
             _tensor(parents, "parents", torch.int32, (T,), dev), T,
             _tensor(query_start, "query_start", torch.int32, (B + 1,), dev), int(max_query_len), B)
-    path = _empty((B, int(max_query_len)), torch.int32, dev, stream)
-    lens = _empty((B,), torch.int32, dev, stream)
-    following = _empty((B,), torch.int64, dev, stream)
-    with _on_device(dev):
-        st = lib().pkv_draft_tree_accept(*args, _dev(path, "accept_path"), _dev(lens, "accept_lens"),
-                                         _dev(following, "next_tokens"), _stream_handle(stream, dev))
+    path = _empty(parents, (B, int(max_query_len)), torch.int32, stream)
+    lens = _empty(parents, (B,), torch.int32, stream)
+    following = _empty(parents, (B,), torch.int64, stream)
+    st = _launch(lib().pkv_draft_tree_accept, dev, stream, *args, path.data_ptr(), lens.data_ptr(), following.data_ptr())
     _check(st, "pkv_draft_tree_accept")
     return path, lens, following
 
@@ -510,7 +528,7 @@ def paged_attention_tree(query: torch.Tensor, query_start: torch.Tensor, max_que
     if key_cache.dim() != 4 or key_cache.shape != value_cache.shape:
         raise ValueError("caches must both be [num_blocks, block_size, num_kv_heads, head_dim]")
     B = _tree_rows(query_start, max_query_len)
-    dev, dt = query.device, _dtype_code(query)
+    dev, dt = _cuda_device(query, "query"), _dtype_code(query)
     T, Hq, D = query.shape
     NB, bs, Hkv, D2 = key_cache.shape
     if D2 != D:
@@ -527,12 +545,13 @@ def paged_attention_tree(query: torch.Tensor, query_start: torch.Tensor, max_que
             _tensor(context_lens, "context_lens", torch.int32, (B,), dev), B, Hq, Hkv, D, bs, NB,
             float(scale))
     if out is None:
-        out = _empty((T, Hq, D), query.dtype, dev, stream)
-    out_ptr = _tensor(out, "out", query.dtype, (T, Hq, D), dev)
+        out = _empty(query, (T, Hq, D), query.dtype, stream)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _tensor(out, "out", query.dtype, (T, Hq, D), dev)
     ws_ptr, ws_bytes, workspace = _scratch(
-        workspace, tree_workspace_bytes(B, int(max_query_len), T, Hq, Hkv, D, MB, bs), dev, stream)
-    with _on_device(dev):
-        st = lib().pkv_paged_attention_tree(*head, ws_ptr, ws_bytes, out_ptr, dt, _stream_handle(stream, dev))
+        query, workspace, tree_workspace_bytes(B, int(max_query_len), T, Hq, Hkv, D, MB, bs), stream)
+    st = _launch(lib().pkv_paged_attention_tree, dev, stream, *head, ws_ptr, ws_bytes, out_ptr, dt)
     _check(st, "pkv_paged_attention_tree")
     return out
 
@@ -557,24 +576,25 @@ def kv_cache_compact(key_caches, value_caches, block_tables: torch.Tensor, start
     first = key_caches[0]
     if first.dim() != 4:
         raise ValueError("caches must be [num_blocks, block_size, num_kv_heads, head_dim]")
-    dev, dt, N = first.device, _dtype_code(first), len(key_caches)
-    NB, bs, Hkv, D = first.shape
+    dev, dt, N = _cuda_device(first, "key_caches"), _dtype_code(first), len(key_caches)
+    NB, bs, Hkv, D = shape = first.shape
     if block_tables.dim() != 2 or keep.dim() != 2:
         raise ValueError("block_tables must be int32 [batch, max_blocks], keep int32 [batch, max_keep]")
     (B, MB), K = block_tables.shape, keep.shape[1]
-    ptrs = [[_tensor(c, name, first.dtype, (NB, bs, Hkv, D), dev) for c in caches]
-            for name, caches in (("key_caches", key_caches), ("value_caches", value_caches))]
-    if len(set(ptrs[0] + ptrs[1])) != 2 * N:
+    ptrs, dtype = [], first.dtype
+    for c in (*key_caches, *value_caches):
+        if c.dtype is not dtype or c.shape != shape or c.device != dev or not c.is_contiguous():
+            raise ValueError("the caches must share one shape, element type and device, and be contiguous")
+        ptrs.append(c.data_ptr())
+    if len(set(ptrs)) != 2 * N:
         raise ValueError("the caches of a call must all be different tensors")
     args = (_tensor(block_tables, "block_tables", torch.int32, (B, MB), dev), MB,
             _tensor(start_lens, "start_lens", torch.int32, (B,), dev),
             _tensor(keep, "keep", torch.int32, (B, K), dev), K,
             _tensor(keep_lens, "keep_lens", torch.int32, (B,), dev), B, Hkv, D, NB, bs)
-    ws_ptr, ws_bytes, workspace = _scratch(workspace, compact_workspace_bytes(N, B, K, Hkv, D), dev, stream)
+    ws_ptr, ws_bytes, workspace = _scratch(first, workspace, compact_workspace_bytes(N, B, K, Hkv, D), stream)
     arr = ctypes.c_void_p * N
-    with _on_device(dev):
-        st = lib().pkv_kv_cache_compact(arr(*ptrs[0]), arr(*ptrs[1]), N, *args, ws_ptr, ws_bytes, dt,
-                                        _stream_handle(stream, dev))
+    st = _launch(lib().pkv_kv_cache_compact, dev, stream, arr(*ptrs[:N]), arr(*ptrs[N:]), N, *args, ws_ptr, ws_bytes, dt)
     _check(st, "pkv_kv_cache_compact")
 
 
