@@ -1296,9 +1296,10 @@ cudaError_t launch_tree(const CUtensorMap &mq, const CacheMaps &cm, const pkv::T
                                cm.k4, cm.v4, a);
     if (e != cudaSuccess)
         return e;
-    const unsigned chunks = (unsigned)((std::min(a.max_query_len * a.group, pkv::kTreeRows) + 31) / 32);
-    return launch_pdl(pkv::tree_merge_kernel<D, BF16>, dim3((unsigned)ctas, chunks, (unsigned)a.shares), dim3(256),
-                      0, st, a);
+    const int sixteens = (std::min(a.max_query_len * a.group, pkv::kTreeRows) + 15) / 16;
+    const int y = std::min(sixteens, std::max(1, 4 * kPlanSmCount / (ctas * a.shares)));   // one wave of CTAs
+    return launch_pdl(pkv::tree_merge_kernel<D, BF16>, dim3((unsigned)ctas, (unsigned)y, (unsigned)a.shares),
+                      dim3(pkv::kTreeMergeThreads), 0, st, a);
 }
 
 template <bool BF16>

@@ -244,7 +244,7 @@ struct TreeArgs {
 constexpr int kTreeThreads = 256;
 constexpr int kTreeRows = 128;           // query rows per tile (MMA M)
 constexpr int kTreeKeys = 64;            // keys per tile
-constexpr int kTreeItemCost = 2;         // an item's start and end, in key tiles
+constexpr int kTreeItemCost = 3;         // an item's start and end, in key tiles
 constexpr int kTreeMinUnits = 2;         // a CTA's share is not cut below this
 
 constexpr int kTreeParts = 6;            // queue of parts between a CTA's warps
@@ -352,9 +352,7 @@ __device__ __forceinline__ int tree_ctas(int total, int most)      // CTAs (or p
 
 // Row r's visible positions p0 .. p0 + 63 as bits: committed cells, and the
 // drafted ones that its mask row names.
-// (mw: the row's first three words, read ahead).
-__device__ __forceinline__ uint64_t tree_bits(const int32_t *mask, const uint32_t (&mw)[3], int words, int base,
-                                              int n, int p0)
+__device__ __forceinline__ uint64_t tree_bits(const int32_t *mask, int words, int base, int n, int p0)
 {
     int j0 = p0 - base;
     uint64_t ones = 0ull;
@@ -370,12 +368,9 @@ __device__ __forceinline__ uint64_t tree_bits(const int32_t *mask, const uint32_
     if (left <= 0)
         return ones;
     const int w = j0 >> 5, o = j0 & 31;
-    uint32_t w0 = mw[0], w1 = mw[1], w2 = mw[2];
-    if (w > 0) {
-        w0 = (uint32_t)__ldg(mask + w);
-        w1 = w + 1 < words ? (uint32_t)__ldg(mask + w + 1) : 0u;
-        w2 = w + 2 < words ? (uint32_t)__ldg(mask + w + 2) : 0u;
-    }
+    const uint32_t w0 = (uint32_t)__ldg(mask + w);
+    const uint32_t w1 = w + 1 < words ? (uint32_t)__ldg(mask + w + 1) : 0u;
+    const uint32_t w2 = w + 2 < words ? (uint32_t)__ldg(mask + w + 2) : 0u;
     uint64_t v = (uint64_t)__funnelshift_r(w0, w1, o) | ((uint64_t)__funnelshift_r(w1, w2, o) << 32);
     if (left < 64)
         v &= (1ull << left) - 1ull;
@@ -406,9 +401,10 @@ __device__ __forceinline__ uint32_t fma_zero2(uint32_t x, uint32_t acc)
 // (they were zeroed in shared memory).  Rare, so simple: one key at a time,
 // read from the cache again.
 template <int D, int BS, bool BF16>
-__device__ __noinline__ void tree_add_nonfinite(const TreeArgs &a, const TreePart &s, int t, uint64_t vis, uint32_t tO)
+__device__ __noinline__ void tree_add_nonfinite(const uint16_t *value_cache, const int32_t *table, int num_blocks,
+                                                int num_kv_heads, int kvh, int len, int t, uint64_t vis, uint32_t tO)
 {
-    const int nblk = (s.len + BS - 1) / BS, tail = s.len % BS;
+    const int nblk = (len + BS - 1) / BS, tail = len % BS;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t o[32];
@@ -421,10 +417,10 @@ __device__ __noinline__ void tree_add_nonfinite(const TreeArgs &a, const TreePar
             const int cell = c % BS - (tail && bi == nblk - 1 ? BS - tail : 0);
             if (cell < 0)
                 continue;
-            int blk = __ldg(a.block_tables + (size_t)s.b * a.max_blocks + bi);
-            blk = (unsigned)blk < (unsigned)a.num_blocks ? blk : 0;
+            int blk = __ldg(table + bi);
+            blk = (unsigned)blk < (unsigned)num_blocks ? blk : 0;
             const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                a.value_cache + (((size_t)blk * BS + cell) * a.num_kv_heads + s.kvh) * D + c0);
+                value_cache + (((size_t)blk * BS + cell) * num_kv_heads + kvh) * D + c0);
             const bool see = (vis >> c) & 1ull;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -485,7 +481,10 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (threadIdx.x < Sh::kNumBars) {
         const int i = threadIdx.x;
         // P: one arrival per softmax warp; a part is read by K, V and MMA warps and the softmax warps
-        const int count = i >= Sh::kPFull && i < Sh::kPFull + 2 ? 4 : (i >= Sh::kPartEmpty ? 7 : 1);
+        // (two Q buffers: a buffer is also where the softmax warps lay out the part's output)
+        const int count = i >= Sh::kPFull && i < Sh::kPFull + 2 ? 4
+                          : i >= Sh::kPartEmpty                 ? 7
+                          : i >= Sh::kQEmpty && i < Sh::kQEmpty + 2 && a.q_slots == 2 ? 5 : 1;
         mbar_init(bar(i), count);
     }
     if (threadIdx.x == 128) {
@@ -675,7 +674,10 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 TreePart p;
                 if (k0 > 0 && k0 < tiles && start >= tree_cut(total, c - 1, n) &&
                     tree_next<BS>(w, a, share, blockIdx.x & 1, &p)) {
-                    int last = c;                    // the last CTA (or pair) with keys of the item
+                    // the last CTA (or pair) with keys of the item: about (its end) n / total
+                    int last = (int)min((int64_t)(n - 1), (int64_t)(start + tiles) * n / total);
+                    while (tree_cut(total, last, n) >= start + tiles)
+                        --last;
                     while (last + 1 < n && tree_cut(total, last + 1, n) < start + tiles)
                         ++last;
                     d = make_int4(p.q0 + p.rt * TT, min(R, p.n * G - p.rt * R), p.kvh, last - c + 2);
@@ -763,11 +765,16 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         ok = false;
                         break;
                     }
+                    // V rows that some query row may not see: from the first drafted
+                    // key on (a shifted last block puts it further on), four at a time
+                    const int i0 = max(0, s.len - s.n - t * kTreeKeys) / 4;
                     uint4 *vt = reinterpret_cast<uint4 *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
                     uint32_t any[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 8
-                    for (int i = 0; i < Sh::kKVBytes / 512; ++i) {
-                        const uint4 x = vt[i * 32];
+#pragma unroll 4
+                    for (int i = i0 * Sh::kHalves; i < Sh::kKVBytes / 512; ++i) {
+                        // (the rows of the 64-column halves in turn)
+                        const int row4 = i / Sh::kHalves, h = i - row4 * Sh::kHalves;
+                        const uint4 x = vt[h * (Sh::kKVHalf / 16) + row4 * 32];
                         any[0] = fma_zero2<BF16>(x.x, any[0]);
                         any[1] = fma_zero2<BF16>(x.y, any[1]);
                         any[2] = fma_zero2<BF16>(x.z, any[2]);
@@ -913,21 +920,21 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool fold = sc > 0.f;                  // a positive scale joins the exponent's fma
         const float sm = fold ? 1.f : sc, se = fold ? sc : 1.f;
         bool ok = true;
-        int J = 0, scans = 0;
-        TreePart s;
-        bool has = next_part(&s, false);
-        while (ok && has) {
-            const int rows = min(R, s.n * G - s.rt * R);      // rows of this tile
-            const bool warp_on = warp * 32 < rows;
-            const bool real = r < rows;
-            const int base = s.len - s.n;
-            const int tail = s.len % BS;
-            const int32_t *mrow = a.tree_mask + (size_t)(s.q0 + s.rt * TT + (real ? r_tok : 0)) * a.words;
-            // the row's first mask words, long before the masked tiles come
-            uint32_t mw[3];
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                mw[i] = i < a.words ? (uint32_t)__ldg(mrow + i) : 0u;
+        int J = 0, scans = 0, u = 0;
+        for (; ok; ++u) {
+            // The part's fields stay in its slot of the queue, which this warp
+            // gives back when it is done: the key loop needs the registers.
+            const int slot = u % kTreeParts;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kPartFull + slot), (uint32_t)((u / kTreeParts) & 1),
+                                                           kWaitLimitNs));
+            const volatile TreePart &s = s_part[slot];
+            const int k1 = s.k1;
+            if (!ok || k1 == 0)
+                break;
+            const int k0 = s.k0;
+            const int first_masked = (s.len - s.n) / kTreeKeys;
+            const int mine = min(R, s.n * G - s.rt * R) - warp * 32;   // this warp's rows of the tile
+            const bool warp_on = mine > 0, real = lane < mine;
             float m_used = kNegInf, l = 0.f;
             uint64_t vis = 0ull;                     // of the last masked tile
             bool was_masked = false;
@@ -935,14 +942,27 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             auto mend = [&](int t) {
                 if (was_masked && *reinterpret_cast<volatile uint32_t *>(&loc->bad[(scans - 1) % kTreeScans])) {
                     if (warp_on)
-                        tree_add_nonfinite<D, BS, BF16>(a, s, t, real ? vis : 0ull, tO + lane_base);
+                        tree_add_nonfinite<D, BS, BF16>(a.value_cache, a.block_tables + (size_t)s.b * a.max_blocks, a.num_blocks,
+                                                        a.num_kv_heads, s.kvh, s.len, t, real ? vis : 0ull, tO + lane_base);
                     __syncwarp();
                 }
             };
-            for (int t = s.k0; t < s.k1; ++t, ++J) {
-                const int t0 = t * kTreeKeys;
+            for (int t = k0; t < k1; ++t, ++J) {
                 const int sb = J & 1;
-                const bool masked = t0 + kTreeKeys > base;
+                const bool masked = t >= first_masked;
+                uint64_t vis_now = ~0ull;
+                if (masked && warp_on) {
+                    const int t0 = t * kTreeKeys, len = s.len, base = len - s.n;
+                    vis_now = tree_bits(a.tree_mask + (size_t)(s.q0 + s.rt * TT + (real ? r_tok : 0)) * a.words, a.words,
+                                        base, len - base, t0);
+                    const int tail = len % BS;
+                    if (t0 + kTreeKeys >= len && tail) {
+                        // the partly filled last block was loaded to end its slot
+                        const int lo = len - tail - t0;
+                        const uint64_t low = (1ull << lo) - 1ull;
+                        vis_now = (vis_now & low) | ((vis_now & ~low) << (BS - tail));
+                    }
+                }
                 ok = mbar_wait_bounded(bar(Sh::kSFull + sb), (uint32_t)((J >> 1) & 1), kWaitLimitNs);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
@@ -952,22 +972,19 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 bool resc = false;
                 float alpha = 1.f;
                 uint32_t pk[32];
-                uint64_t vis_now = ~0ull;
                 if (warp_on) {
                     uint32_t raw[64];
                     tmem_ld64(tmem + lane_base + sb * kTreeKeys, raw);
                     float x[64];
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
-                        x[c] = fold ? __uint_as_float(raw[c]) : __uint_as_float(raw[c]) * sm;
+                        x[c] = __uint_as_float(raw[c]);
+                    if (!fold) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            x[c] *= sm;
+                    }
                     if (masked) {
-                        vis_now = tree_bits(mrow, mw, a.words, base, s.n, t0);
-                        if (t + 1 == s.tiles && tail) {
-                            // the partly filled last block was loaded to end its slot
-                            const int lo = s.len - tail - t0;
-                            const uint64_t low = (1ull << lo) - 1ull;
-                            vis_now = (vis_now & low) | ((vis_now & ~low) << (BS - tail));
-                        }
                         const uint32_t vlo = (uint32_t)vis_now, vhi = (uint32_t)(vis_now >> 32);
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
@@ -999,7 +1016,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     l = l * alpha + (f2_lo(r2) + f2_hi(r2));
                     m_used = m_new;
                 }
-                if (t > s.k0) {
+                if (t > k0) {
                     // P_{J-1} V_{J-1} has completed: O is stable, and O_DONE within one phase
                     ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
                     if (!__all_sync(0xffffffffu, ok)) {
@@ -1034,17 +1051,68 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (!ok)
                 break;
-            TreePart nx;                             // read while the last P V runs
-            has = next_part(&nx, false);
+            const bool item = k0 == 0 && k1 == s.tiles;
             const size_t orow = (size_t)(s.q0 + s.rt * TT + r_tok) * a.num_heads + (size_t)s.kvh * G + r_head;
             const float inv = l == 0.f ? 0.f : __frcp_rn(l);
             ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
             ok = __all_sync(0xffffffffu, ok);
+            const bool whole = item && two_q;
+            // this warp is done with the part's Q buffer
+            auto release_q = [&]() {
+                if (two_q) {
+                    fence_proxy_async_smem();        // before the next Q is copied over laid-out rows
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(Sh::kQEmpty + (u & 1)));
+                }
+            };
             if (ok && warp_on) {
                 tc_fence_after();
-                mend(s.k1 - 1);
-                if (s.k0 == 0 && s.k1 == s.tiles) {
-                    // the whole item: output rows
+                mend(k1 - 1);
+                if (whole) {
+                    // The whole item: output rows, laid out in the part's Q
+                    // buffer (its last S has been read), so that a store
+                    // covers 128 bytes of each of four rows and not 16 of 32.
+                    uint8_t *lay = data + (u & 1) * 64 * 128 + warp * 32 * 128;
+#pragma unroll
+                    for (int h = 0; h < Sh::kHalves; ++h) {
+                        uint32_t o[64];
+                        tmem_ld64(tO + lane_base + h * 64, o);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack2<BF16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                                   __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(lay + h * Sh::kQHalf + lane * 128 + ((v ^ (lane & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    __syncwarp();
+                    const int c = lane & 7, r0 = lane >> 3;
+                    uint4 x[Sh::kHalves][8];
+#pragma unroll
+                    for (int h = 0; h < Sh::kHalves; ++h)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            x[h][i] = *reinterpret_cast<const uint4 *>(lay + h * Sh::kQHalf + (i * 4 + r0) * 128 +
+                                                                       ((c ^ ((i * 4 + r0) & 7)) << 4));
+                    release_q();                     // before the stores, which the fence would wait for
+                    uint16_t *const o0 = a.out + ((size_t)(s.q0 + s.rt * TT) * a.num_heads + (size_t)s.kvh * G) * D + c * 8;
+                    const uint32_t skip = (uint32_t)(a.num_heads - G), div_g = (65536u + G - 1) / G;   // rr / G = rr div_g >> 16 (rr < 128)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t rr = warp * 32 + i * 4 + r0;
+                        if (i * 4 + r0 < mine) {
+                            // row (token rr / G, head rr % G)
+                            uint4 *to = reinterpret_cast<uint4 *>(o0 + (size_t)((rr * div_g >> 16) * skip + rr) * D);
+#pragma unroll
+                            for (int h = 0; h < Sh::kHalves; ++h)
+                                to[h * 8] = x[h][i];
+                        }
+                    }
+                } else if (item) {
                     uint4 *o16 = reinterpret_cast<uint4 *>(a.out + orow * D);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 64) {
@@ -1064,7 +1132,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 } else {
                     // a part of an item: a record (m, l, O), part 1 if the item starts here
-                    const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (s.k0 > 0 ? 0 : 1)) * kTreeRows + r;
+                    const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (k0 > 0 ? 0 : 1)) * kTreeRows + r;
                     float4 *orec = reinterpret_cast<float4 *>(a.rec_o + rec * D);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
@@ -1081,7 +1149,11 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         a.rec_ml[rec] = make_float2(m_used, l);
                 }
             }
-            s = nx;
+            if (!(whole && warp_on))
+                release_q();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(Sh::kPartEmpty + slot));
             // the next part's first P V overwrites O after this warp's next P
         }
         if (!ok && lane == 0)
@@ -1099,54 +1171,80 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
 // The records of an item that several CTAs shared, joined by log-sum-exp:
 //   out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,   M = max_k m_k.
-// CTA (c, x, share) takes rows 32 x .. 32 x + 31 of the item whose second part
-// opens CTA c's share; a warp takes a row, a lane D / 32 of its columns.
+// The CTAs (c, y, share) take the rows of the item whose second part opens CTA
+// c's share, sixteen to a CTA at a time; a warp takes two rows side by side, a
+// lane D / 32 of their columns.  Bound by the round trips, so four records are
+// loaded at a time; small enough that all CTAs, most of which have nothing to
+// join, run at once.
+constexpr int kTreeMergeThreads = 256;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kTreeMergeThreads, 4)
 tree_merge_kernel(const TreeArgs a)
 {
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, B = 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int c = blockIdx.x, share = blockIdx.z;
     const int4 d = __ldg(a.desc + c * 2 + share);
     const int step = a.shares == 2 && share == 0 ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (d.w == 0)
-        return;
-    for (int r = blockIdx.y * 32 + warp; r < min(d.y, (int)(blockIdx.y + 1) * 32); r += 8) {
-        // record k: CTA c + (k - 1) step; part 1 of the first, part 0 of the others
-        auto rec = [&](int k) {
-            return (((size_t)(c + (k - 1) * step) * 2 + share) * 2 + (k == 0 ? 1 : 0)) * kTreeRows + r;
-        };
-        float M = kNegInf;
-        for (int k = lane; k < d.w; k += 32)
-            M = fmaxf(M, __ldg(&a.rec_ml[rec(k)].x));
+    for (int r0 = ((int)blockIdx.y * 8 + warp) * 2; r0 < d.y; r0 += (int)gridDim.y * 16) {   // (no records: d.y is 0)
+    // record k: CTA c + (k - 1) step; part 1 of the first, part 0 of the others
+    auto rec = [&](int k) {
+        return (((size_t)(c + (k - 1) * step) * 2 + share) * 2 + (k == 0 ? 1 : 0)) * kTreeRows + r0;
+    };
+    const int second = r0 + 1 < d.y ? 1 : 0;      // (an odd last row is taken twice)
+    float M[2] = {kNegInf, kNegInf};
+    for (int k = lane; k < d.w; k += 32) {
+        M[0] = fmaxf(M[0], __ldg(&a.rec_ml[rec(k)].x));
+        M[1] = fmaxf(M[1], __ldg(&a.rec_ml[rec(k) + second].x));
+    }
 #pragma unroll
-        for (int o = 16; o; o >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float den = 0.f, acc[V];
+    for (int o = 16; o; o >>= 1) {
+        M[0] = fmaxf(M[0], __shfl_xor_sync(0xffffffffu, M[0], o));
+        M[1] = fmaxf(M[1], __shfl_xor_sync(0xffffffffu, M[1], o));
+    }
+    float den[2] = {0.f, 0.f}, acc[2][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            acc[i] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < d.w; ++k) {
-            const float2 ml = __ldg(a.rec_ml + rec(k));
-            float v[V];
-            load_slice<D>(a.rec_o + rec(k) * D + lane * V, v);
-            const float f = ml.x == kNegInf ? 1.f : ex2(ml.x - M);   // (1: a part without keys, or all NaN)
-            den += f * ml.y;
+    for (int i = 0; i < V; ++i)
+        acc[0][i] = acc[1][i] = 0.f;
+    for (int k0 = 0; k0 < d.w; k0 += B) {
+        float2 ml[B][2];
+        float v[B][2][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                acc[i] += f * v[i];
-        }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const size_t at = rec(min(k0 + j, d.w - 1)) + (q ? second : 0);
+                ml[j][q] = __ldg(a.rec_ml + at);
+                load_slice<D>(a.rec_o + at * D + lane * V, v[j][q]);
+            }
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (k0 + j < d.w) {
+                    // (1: a part without keys, or all NaN)
+                    const float f = ml[j][q].x == kNegInf ? 1.f : ex2(ml[j][q].x - M[q]);
+                    den[q] += f * ml[j][q].y;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        acc[q][i] += f * v[j][q][i];
+                }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = r0 + q;
+        if (r >= d.y)
+            break;
+        const float inv = den[q] == 0.f ? 0.f : 1.f / den[q];
         uint16_t *o = a.out + ((size_t)(d.x + r / a.group) * a.num_heads + (size_t)d.z * a.group + r % a.group) * D + lane * V;
         if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),
-                                                       pack2<BF16>(acc[2] * inv, acc[3] * inv));
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv),
+                                                       pack2<BF16>(acc[q][2] * inv, acc[q][3] * inv));
         else
-            *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+            *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv);
+    }
     }
 }
 
@@ -1424,8 +1522,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 vis[mt][h] = 0xffffffffu;
                 if (masked) {
                     const int32_t *mrow = a.tree_mask + (size_t)(s.q0 + node[mt][h]) * a.words;
-                    const uint32_t mw[3] = {(uint32_t)__ldg(mrow), a.words > 1 ? (uint32_t)__ldg(mrow + 1) : 0u, 0u};
-                    vis[mt][h] = (uint32_t)tree_bits(mrow, mw, a.words, base, s.n, p0);
+                    vis[mt][h] = (uint32_t)tree_bits(mrow, a.words, base, s.n, p0);
                 }
                 float mx = kNegInf;
 #pragma unroll
