@@ -1218,7 +1218,9 @@ namespace {
 struct TreePlan {
     int few;                    // 16-row tiles per item of the few-rows kernel (1, 2), 0: the 128-row tiles
     int part_tokens, parts;     // few rows: keys of a part, parts of the longest item
-    int ctas, shares;           // 128-row tiles
+    int cluster;                // 128-row tiles: CTAs per item of a small call, 0: shares
+    int row_tiles;
+    int ctas, shares;
     size_t ml, o, total;        // workspace offsets (128-row tiles: the descriptors come first)
 };
 #ifndef PKV_TUNE_FEW
@@ -1253,9 +1255,22 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
     }
     const int per_tile = pkv::kTreeRows / (num_heads / num_kv_heads);
     const int row_tiles = (max_query_len + per_tile - 1) / per_tile;
+    p.row_tiles = std::max(1, row_tiles);
+    // Small calls, one wave of CTAs of at most eight key tiles each: clusters of
+    // 1, 2, 4 or 8 CTAs per item.
+    const int64_t tiles = ((int64_t)max_blocks * block_size + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
+    const int64_t items = (int64_t)batch * num_kv_heads * p.row_tiles;
+    if (items <= 2 * kPlanSmCount) {
+        int size = 1;
+        while (size < 8 && items * size * 2 <= 2 * kPlanSmCount && size < tiles)
+            size *= 2;
+        if (tiles <= 8 * size) {
+            p.cluster = size;
+            return p;
+        }
+    }
     p.shares = row_tiles > 1 ? 2 : 1;
     // two CTAs per SM, fewer where the largest such call has less to share out
-    const int64_t tiles = ((int64_t)max_blocks * block_size + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
     const int64_t units = (int64_t)batch * num_kv_heads * std::max(1, row_tiles) * (tiles + pkv::kTreeItemCost);
     if (units >= (int64_t)1 << 31) {
         p.ctas = 0;             // more than a call's shares are counted in
@@ -1270,46 +1285,70 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
     return p;
 }
 
-template <int D, int BS, bool BF16>
-cudaError_t launch_tree(const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a, int ctas,
-                        cudaStream_t st)
+template <int D, int BS, bool BF16, bool CL>
+cudaError_t configure_tree()
 {
-    constexpr int smem = pkv::TreeShape<D>::kSmemBytes;
-    auto kern = pkv::tree_attend_kernel<D, BS, BF16>;
+    auto kern = pkv::tree_attend_kernel<D, BS, BF16, CL>;
     static bool configured[64] = {};
     static std::mutex mu;
     const int dev = current_device();
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (dev < 0 || dev >= 64 || !configured[dev]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e == cudaSuccess)   // two CTAs (and their TMEM) per SM
-                e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         cudaSharedmemCarveoutMaxShared);
-            if (e != cudaSuccess)
-                return e;
-            if (dev >= 0 && dev < 64)
-                configured[dev] = true;
-        }
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev >= 0 && dev < 64 && configured[dev])
+        return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         pkv::TreeShape<D>::kSmemBytes);
+    if (e == cudaSuccess)   // two CTAs (and their TMEM) per SM
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev >= 0 && dev < 64)
+        configured[dev] = true;
+    return e;
+}
+
+template <int D, int BS, bool BF16>
+cudaError_t launch_tree(const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a, const TreePlan &plan,
+                        cudaStream_t st)
+{
+    constexpr int smem = pkv::TreeShape<D>::kSmemBytes;
+    if (plan.cluster) {
+        cudaError_t e = configure_tree<D, BS, BF16, true>();
+        if (e != cudaSuccess)
+            return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)plan.cluster, (unsigned)(a.batch * a.num_kv_heads * a.row_tiles));
+        cfg.blockDim = dim3(pkv::kTreeThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)plan.cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, pkv::tree_attend_kernel<D, BS, BF16, true>, mq, cm.k, cm.v, cm.k4, cm.v4, a);
     }
-    cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(pkv::kTreeThreads), smem, st, mq, cm.k, cm.v,
-                               cm.k4, cm.v4, a);
+    cudaError_t e = configure_tree<D, BS, BF16, false>();
+    if (e == cudaSuccess)
+        e = launch_pdl(pkv::tree_attend_kernel<D, BS, BF16, false>, dim3((unsigned)plan.ctas), dim3(pkv::kTreeThreads),
+                       smem, st, mq, cm.k, cm.v, cm.k4, cm.v4, a);
     if (e != cudaSuccess)
         return e;
     const int sixteens = (std::min(a.max_query_len * a.group, pkv::kTreeRows) + 15) / 16;
-    const int y = std::min(sixteens, std::max(1, 4 * kPlanSmCount / (ctas * a.shares)));   // one wave of CTAs
-    return launch_pdl(pkv::tree_merge_kernel<D, BF16>, dim3((unsigned)ctas, (unsigned)y, (unsigned)a.shares),
+    return launch_pdl(pkv::tree_merge_kernel<D, BF16>, dim3((unsigned)plan.ctas, (unsigned)std::min(sixteens, 4)),
                       dim3(pkv::kTreeMergeThreads), 0, st, a);
 }
 
 template <bool BF16>
 cudaError_t dispatch_tree(int D, int bs, const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a,
-                          int ctas, cudaStream_t st)
+                          const TreePlan &plan, cudaStream_t st)
 {
-    if (D == 64 && bs == 16) return launch_tree<64, 16, BF16>(mq, cm, a, ctas, st);
-    if (D == 64 && bs == 32) return launch_tree<64, 32, BF16>(mq, cm, a, ctas, st);
-    if (D == 128 && bs == 16) return launch_tree<128, 16, BF16>(mq, cm, a, ctas, st);
-    return launch_tree<128, 32, BF16>(mq, cm, a, ctas, st);
+    if (D == 64 && bs == 16) return launch_tree<64, 16, BF16>(mq, cm, a, plan, st);
+    if (D == 64 && bs == 32) return launch_tree<64, 32, BF16>(mq, cm, a, plan, st);
+    if (D == 128 && bs == 16) return launch_tree<128, 16, BF16>(mq, cm, a, plan, st);
+    return launch_tree<128, 32, BF16>(mq, cm, a, plan, st);
 }
 
 }  // namespace
@@ -1408,7 +1447,7 @@ extern "C" pkv_status pkv_paged_attention_tree(
         return fail(PKV_ERR_MISALIGNED, "query_start/tree_mask/block_tables/context_lens must be 4-byte aligned");
     const TreePlan plan =
         tree_plan(batch, max_query_len, num_heads, num_kv_heads, head_dim, max_blocks, block_size, num_tokens);
-    if (!plan.few && plan.ctas == 0)
+    if (!plan.few && !plan.cluster && plan.ctas == 0)
         return fail(PKV_ERR_UNSUPPORTED, "batch x num_kv_heads x row tiles x key tiles is 2^31 or more");
     if (plan.total > 0 && (!workspace || workspace_bytes < plan.total))
         return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.total,
@@ -1481,11 +1520,12 @@ extern "C" pkv_status pkv_paged_attention_tree(
     a.num_kv_heads = num_kv_heads;
     a.group = group;
     a.num_blocks = (int)num_blocks;
+    a.row_tiles = plan.row_tiles;
     a.shares = plan.shares;
     a.q_slots = two_q ? 2 : 1;
     a.scale_log2 = scale_log2;
-    const cudaError_t e = dtype == PKV_BF16 ? dispatch_tree<true>(head_dim, block_size, mq, cm, a, plan.ctas, st)
-                                            : dispatch_tree<false>(head_dim, block_size, mq, cm, a, plan.ctas, st);
+    const cudaError_t e = dtype == PKV_BF16 ? dispatch_tree<true>(head_dim, block_size, mq, cm, a, plan, st)
+                                            : dispatch_tree<false>(head_dim, block_size, mq, cm, a, plan, st);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_attend_kernel launch");
     return PKV_OK;

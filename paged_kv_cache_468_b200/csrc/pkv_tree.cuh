@@ -9,6 +9,8 @@
 // smaller one than its own, or -1.
 #pragma once
 
+#include <type_traits>
+
 #include "pkv_prefill.cuh"
 
 namespace pkv {
@@ -213,6 +215,12 @@ tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict_
 // read comes from L2); an odd last row tile joins the single ones.  Pairs and
 // singles are two such sequences of units, shared out one after the other.
 //
+// Calls with little to do in all are bound by latency: working out the shares
+// and a second kernel would cost as much as the attention.  There (CL) a
+// cluster of 1, 2, 4 or 8 CTAs takes an item, a CTA an equal run of its key
+// tiles, and the partial results are joined through the cluster's shared
+// memory: one kernel, no workspace.
+//
 // A masked tile is the only one whose V rows some row may not see: such a row
 // gives them weight 0, and 0 times an infinity or a NaN would poison it.  The
 // softmax warps look through the V rows of masked tiles; where one holds such
@@ -236,6 +244,7 @@ struct TreeArgs {
     int num_kv_heads;
     int group;
     int num_blocks;
+    int row_tiles;                   // of the largest tree (CL: items are (sequence, kv head, row tile))
     int shares;                      // 2: pairs of row tiles, then single ones; 1: single ones only
     int q_slots;                     // 2: two Q buffers of 64 rows (no item has more), 1: one of 128
     float scale_log2;
@@ -441,7 +450,35 @@ __device__ __noinline__ void tree_add_nonfinite(const uint16_t *value_cache, con
 // Warps: 0-3 softmax and output (warp w owns TMEM lanes 32 w ..), 4 K loads,
 // 5 MMA issue, 6 V loads, 7 the parts' queue, Q loads and the scan of masked
 // tiles' V rows.
-template <int D, int BS, bool BF16>
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `addr` (own shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int D, int BS, bool BF16, bool CL>
 __global__ void __launch_bounds__(kTreeThreads, 2)
 tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k4,
@@ -481,10 +518,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (threadIdx.x < Sh::kNumBars) {
         const int i = threadIdx.x;
         // P: one arrival per softmax warp; a part is read by K, V and MMA warps and the softmax warps
-        // (two Q buffers: a buffer is also where the softmax warps lay out the part's output)
-        const int count = i >= Sh::kPFull && i < Sh::kPFull + 2 ? 4
-                          : i >= Sh::kPartEmpty                 ? 7
-                          : i >= Sh::kQEmpty && i < Sh::kQEmpty + 2 && a.q_slots == 2 ? 5 : 1;
+        const int count = i >= Sh::kPFull && i < Sh::kPFull + 2 ? 4 : (i >= Sh::kPartEmpty ? 7 : 1);
         mbar_init(bar(i), count);
     }
     if (threadIdx.x == 128) {
@@ -509,9 +543,40 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
+    int cl_tiles = 0, cl_rows = 0, cl_q0 = 0, cl_kvh = 0;   // CL: the item, if it is joined (else cl_rows is 0)
+    if constexpr (CL) {
+        // ---- the CTA's one part: key tiles tiles x / P .. tiles (x + 1) / P - 1 of item y ----
+        const int item = blockIdx.y, P = gridDim.x;
+        const int bh = item / a.row_tiles, rt = item - bh * a.row_tiles;
+        const int b = bh / a.num_kv_heads, kvh = bh - b * a.num_kv_heads;
+        TreeSeq q;
+        const bool good = tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &q);
+        if (!good && threadIdx.x == 0 && blockIdx.x == 0 && rt == 0 && kvh == 0)
+            raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
+        const int rows = good ? min(R, q.n * G - rt * R) : 0;
+        const int tiles = rows > 0 ? (q.len + kTreeKeys - 1) / kTreeKeys : 0;
+        if (threadIdx.x == 0) {
+            TreePart p{b, kvh, rt, 0, q.q0, q.n, q.len, tiles, tiles * (int)blockIdx.x / P, tiles * ((int)blockIdx.x + 1) / P};
+            if (p.k0 == p.k1)
+                p.k1 = 0;
+            loc->part[0] = p;
+            loc->part[1].k1 = 0;
+            mbar_arrive(bar(Sh::kPartFull));
+            mbar_arrive(bar(Sh::kPartFull + 1));
+        }
+        if (P > 1 && tiles > 1) {                    // (a single tile is one CTA's alone)
+            cl_tiles = tiles;
+            cl_rows = rows;
+            cl_q0 = q.q0 + rt * TT;
+            cl_kvh = kvh;
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
     // ---- this CTA's shares: a thread adds up a run of sequences, the block
     // their totals; the thread whose run holds the share's start finds it ----
-    for (int share = 0; share < a.shares; ++share) {
+    for (int share = 0; !CL && share < a.shares; ++share) {
         const bool pair = a.shares == 2 && share == 0;
         const int per = (a.batch + kTreeThreads - 1) / kTreeThreads;
         const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
@@ -606,7 +671,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         TreePart s;
         while (ok && next_part(&s, false)) {
             // a pair's keys are read a second time, by the other CTA
-            const uint64_t policy = a.shares == 2 && s.share == 0 ? again : once;
+            const uint64_t policy = (CL ? a.row_tiles > 1 : a.shares == 2 && s.share == 0) ? again : once;
             const int nblk = (s.len + BS - 1) / BS;
             const int tail = s.len % BS;
             const int32_t *trow = a.block_tables + (size_t)s.b * a.max_blocks;
@@ -656,7 +721,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (lane == 0)
             for (int j = J > NS ? J - NS : 0; j < J; ++j)
                 mbar_wait_bounded(bar(full0 + j % NS), (uint32_t)((j / NS) & 1), kWaitLimitNs / 8);
-        if (is_k && lane < a.shares) {
+        if (!CL && is_k && lane < a.shares) {
             // An item that started in the share before and goes on in this one:
             // the merge finds its records through this share.
             const int share = lane;
@@ -691,9 +756,9 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // here: the loaders run at most their rings ahead of the MMAs.
         constexpr int kAhead = 4;
         const uint64_t policy = policy_evict_normal();
-        TreeWalk walk = loc->walk[0];
-        int share = 0, made = 0, scans = 0, vs = 0, vround = 0;
-        bool ok = true, done = false;
+        TreeWalk walk = CL ? TreeWalk{} : loc->walk[0];
+        int share = 0, made = CL ? 2 : 0, scans = 0, vs = 0, vround = 0;
+        bool ok = true, done = CL;
         auto make = [&]() {                          // queue part `made`
             const int slot = made % kTreeParts;
             if (made >= kTreeParts &&
@@ -1056,63 +1121,11 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const float inv = l == 0.f ? 0.f : __frcp_rn(l);
             ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
             ok = __all_sync(0xffffffffu, ok);
-            const bool whole = item && two_q;
-            // this warp is done with the part's Q buffer
-            auto release_q = [&]() {
-                if (two_q) {
-                    fence_proxy_async_smem();        // before the next Q is copied over laid-out rows
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar(Sh::kQEmpty + (u & 1)));
-                }
-            };
             if (ok && warp_on) {
                 tc_fence_after();
                 mend(k1 - 1);
-                if (whole) {
-                    // The whole item: output rows, laid out in the part's Q
-                    // buffer (its last S has been read), so that a store
-                    // covers 128 bytes of each of four rows and not 16 of 32.
-                    uint8_t *lay = data + (u & 1) * 64 * 128 + warp * 32 * 128;
-#pragma unroll
-                    for (int h = 0; h < Sh::kHalves; ++h) {
-                        uint32_t o[64];
-                        tmem_ld64(tO + lane_base + h * 64, o);
-#pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack2<BF16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                                   __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(lay + h * Sh::kQHalf + lane * 128 + ((v ^ (lane & 7)) << 4)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                    __syncwarp();
-                    const int c = lane & 7, r0 = lane >> 3;
-                    uint4 x[Sh::kHalves][8];
-#pragma unroll
-                    for (int h = 0; h < Sh::kHalves; ++h)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            x[h][i] = *reinterpret_cast<const uint4 *>(lay + h * Sh::kQHalf + (i * 4 + r0) * 128 +
-                                                                       ((c ^ ((i * 4 + r0) & 7)) << 4));
-                    release_q();                     // before the stores, which the fence would wait for
-                    uint16_t *const o0 = a.out + ((size_t)(s.q0 + s.rt * TT) * a.num_heads + (size_t)s.kvh * G) * D + c * 8;
-                    const uint32_t skip = (uint32_t)(a.num_heads - G), div_g = (65536u + G - 1) / G;   // rr / G = rr div_g >> 16 (rr < 128)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t rr = warp * 32 + i * 4 + r0;
-                        if (i * 4 + r0 < mine) {
-                            // row (token rr / G, head rr % G)
-                            uint4 *to = reinterpret_cast<uint4 *>(o0 + (size_t)((rr * div_g >> 16) * skip + rr) * D);
-#pragma unroll
-                            for (int h = 0; h < Sh::kHalves; ++h)
-                                to[h * 8] = x[h][i];
-                        }
-                    }
-                } else if (item) {
+                if (item) {
+                    // the whole item: output rows
                     uint4 *o16 = reinterpret_cast<uint4 *>(a.out + orow * D);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 64) {
@@ -1131,7 +1144,24 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                     }
                 } else {
-                    // a part of an item: a record (m, l, O), part 1 if the item starts here
+                    // a part of an item: a record (m, l, O); CL: in shared memory, over
+                    // the K and V rings (every copy and product is done), 16-byte
+                    // chunks of a row swizzled by the row
+                    if constexpr (CL) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + lane_base + c0, o);
+#pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                *reinterpret_cast<uint4 *>(data + Sh::kKOff + r * D * 4 + (((c0 / 4 + v) ^ (r & 7)) << 4)) =
+                                    make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                        }
+                        *reinterpret_cast<float2 *>(data + r * 8) = make_float2(m_used, l);   // (over Q)
+                        __syncwarp();
+                        continue;
+                    }
+                    // (part 1 if the item starts here)
                     const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (k0 > 0 ? 0 : 1)) * kTreeRows + r;
                     float4 *orec = reinterpret_cast<float4 *>(a.rec_o + rec * D);
 #pragma unroll 1
@@ -1149,8 +1179,6 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         a.rec_ml[rec] = make_float2(m_used, l);
                 }
             }
-            if (!(whole && warp_on))
-                release_q();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar(Sh::kPartEmpty + slot));
@@ -1167,27 +1195,83 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if constexpr (CL) {
+        if (cl_rows == 0)
+            return;                                  // (so for the whole cluster)
+        // ---- join the cluster's parts by log-sum-exp: a warp to a row, a lane
+        // to D / 32 of its columns, all parts' loads at once ----
+        cluster_barrier();
+        constexpr int V = D / 32;
+        const int P = gridDim.x, rank = blockIdx.x;
+        for (int r = rank * 8 + warp; r < cl_rows; r += P * 8) {
+            const uint32_t at_ml = data_s + r * 8;
+            const uint32_t at_o = data_s + Sh::kKOff + r * D * 4 + (((lane * V / 4) ^ (r & 7)) << 4) + (lane * V % 4) * 4;
+            float2 ml[8];
+            float v[8][V];
+            float M = kNegInf;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                // part k has keys
+                if (k < P && cl_tiles * k / P < cl_tiles * (k + 1) / P) {
+                    ml[k] = cluster_load2(cluster_map(at_ml, k));
+                    if constexpr (V == 4) {
+                        const float4 x = cluster_load4(cluster_map(at_o, k));
+                        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                    } else {
+                        const float2 x = cluster_load2(cluster_map(at_o, k));
+                        v[k][0] = x.x, v[k][1] = x.y;
+                    }
+                } else {
+                    ml[k] = make_float2(kNegInf, 0.f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        v[k][i] = 0.f;
+                }
+                M = fmaxf(M, ml[k].x);
+            }
+            float den = 0.f, acc[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                acc[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                // (1: no keys seen, or all NaN)
+                const float f = ml[k].x == kNegInf ? 1.f : ex2(ml[k].x - M);
+                den += f * ml[k].y;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    acc[i] += f * v[k][i];
+            }
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            uint16_t *o = a.out + ((size_t)(cl_q0 + r / G) * a.num_heads + (size_t)cl_kvh * G + r % G) * D + lane * V;
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),
+                                                           pack2<BF16>(acc[2] * inv, acc[3] * inv));
+            else
+                *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+        }
+        cluster_barrier();                           // no CTA leaves while its memory is read
+    }
 }
 
 // The records of an item that several CTAs shared, joined by log-sum-exp:
 //   out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,   M = max_k m_k.
-// The CTAs (c, y, share) take the rows of the item whose second part opens CTA
-// c's share, sixteen to a CTA at a time; a warp takes two rows side by side, a
+// The CTAs (c, y) take the rows of the items whose second parts open CTA c's
+// shares, sixteen to a CTA at a time; a warp takes two rows side by side, a
 // lane D / 32 of their columns.  Bound by the round trips, so four records are
-// loaded at a time; small enough that all CTAs, most of which have nothing to
-// join, run at once.
+// loaded at a time; many of the CTAs have nothing to join.
 constexpr int kTreeMergeThreads = 256;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kTreeMergeThreads, 4)
 tree_merge_kernel(const TreeArgs a)
 {
-    constexpr int V = D / 32, B = 4;
+    constexpr int V = D / 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int c = blockIdx.x, share = blockIdx.z;
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int share = 0; share < a.shares; ++share) {
     const int4 d = __ldg(a.desc + c * 2 + share);
     const int step = a.shares == 2 && share == 0 ? 2 : 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int r0 = ((int)blockIdx.y * 8 + warp) * 2; r0 < d.y; r0 += (int)gridDim.y * 16) {   // (no records: d.y is 0)
     // record k: CTA c + (k - 1) step; part 1 of the first, part 0 of the others
     auto rec = [&](int k) {
@@ -1208,30 +1292,39 @@ tree_merge_kernel(const TreeArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i)
         acc[0][i] = acc[1][i] = 0.f;
-    for (int k0 = 0; k0 < d.w; k0 += B) {
-        float2 ml[B][2];
-        float v[B][2][V];
+    auto batch = [&](auto count, int k0) {           // records k0 .. k0 + N - 1
+        constexpr int N = decltype(count)::value;
+        float2 ml[N][2];
+        float v[N][2][V];
 #pragma unroll
-        for (int j = 0; j < B; ++j)
+        for (int j = 0; j < N; ++j)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const size_t at = rec(min(k0 + j, d.w - 1)) + (q ? second : 0);
+                const size_t at = rec(k0 + j) + (q ? second : 0);
                 ml[j][q] = __ldg(a.rec_ml + at);
                 load_slice<D>(a.rec_o + at * D + lane * V, v[j][q]);
             }
 #pragma unroll
-        for (int j = 0; j < B; ++j)
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (k0 + j < d.w) {
-                    // (1: a part without keys, or all NaN)
-                    const float f = ml[j][q].x == kNegInf ? 1.f : ex2(ml[j][q].x - M[q]);
-                    den[q] += f * ml[j][q].y;
+            for (int q = 0; q < 2; ++q) {
+                // (1: a part without keys, or all NaN)
+                const float f = ml[j][q].x == kNegInf ? 1.f : ex2(ml[j][q].x - M[q]);
+                den[q] += f * ml[j][q].y;
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        acc[q][i] += f * v[j][q][i];
-                }
-    }
+                for (int i = 0; i < V; ++i)
+                    acc[q][i] += f * v[j][q][i];
+            }
+    };
+    int k0 = 0;
+    for (; k0 + 4 <= d.w; k0 += 4)
+        batch(std::integral_constant<int, 4>{}, k0);
+    if (d.w - k0 == 3)
+        batch(std::integral_constant<int, 3>{}, k0);
+    else if (d.w - k0 == 2)
+        batch(std::integral_constant<int, 2>{}, k0);
+    else if (d.w - k0 == 1)
+        batch(std::integral_constant<int, 1>{}, k0);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int r = r0 + q;
@@ -1244,6 +1337,7 @@ tree_merge_kernel(const TreeArgs a)
                                                        pack2<BF16>(acc[q][2] * inv, acc[q][3] * inv));
         else
             *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv);
+    }
     }
     }
 }
