@@ -1216,34 +1216,52 @@ namespace {
 
 // CTAs of a tree attention call and the layout of its records.
 struct TreePlan {
-    int few;                    // 16-row tiles per item of the few-rows kernel (1, 2), 0: the 128-row tiles
+    bool few;                   // the few-rows kernel
     int part_tokens, parts;     // few rows: keys of a part, parts of the longest item
     int cluster;                // 128-row tiles: CTAs per item of a small call, 0: shares
     int row_tiles;
     int ctas, shares;
     size_t ml, o, total;        // workspace offsets (128-row tiles: the descriptors come first)
 };
-#ifndef PKV_TUNE_FEW
-#define PKV_TUNE_FEW 16
-#endif
-#ifndef PKV_TUNE_PARTS
-#define PKV_TUNE_PARTS 592
-#endif
-#ifndef PKV_TUNE_MAXPART
-#define PKV_TUNE_MAXPART 512
-#endif
 TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
                    int max_blocks, int block_size, int num_tokens)
 {
     TreePlan p = {};
-    const int rows_per_item = max_query_len * (num_heads / num_kv_heads);
-    if (rows_per_item <= PKV_TUNE_FEW) {
-        p.few = rows_per_item <= 16 ? 1 : 2;
-        const int64_t span = (int64_t)max_blocks * block_size;
-        const int64_t items = (int64_t)batch * num_kv_heads;
-        int64_t parts = (PKV_TUNE_PARTS + items - 1) / items;           // enough CTAs
-        parts = std::max(parts, span >= 2048 ? (span + PKV_TUNE_MAXPART - 1) / PKV_TUNE_MAXPART : (int64_t)1);
-        const int64_t unit = std::max(64, block_size);
+    const int group = num_heads / num_kv_heads;
+    const int per_tile = pkv::kTreeRows / group;
+    const int row_tiles = std::max(1, (max_query_len + per_tile - 1) / per_tile);
+    const int64_t span = (int64_t)max_blocks * block_size;
+    const int64_t tiles = (span + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
+    const int64_t items = (int64_t)batch * num_kv_heads;
+    const bool few = max_query_len * group <= 16;
+    p.row_tiles = row_tiles;
+    // Small calls, one wave of CTAs of at most eight key tiles each: clusters of
+    // 1, 2, 4 or 8 CTAs per item (8 sequences of 600 tokens, 4 nodes of 32/8
+    // heads: 11.8 us, by the few-rows kernel 14.4, by shares 20).  Up to 16
+    // rows the few-rows kernel is ahead where an item is one CTA's.
+    if (items * row_tiles <= 2 * kPlanSmCount) {
+        int size = 1;
+        while (size < 8 && items * row_tiles * size * 2 <= 2 * kPlanSmCount && size < tiles)
+            size *= 2;
+        if (tiles <= 8 * size && !(few && size == 1)) {
+            p.cluster = size;
+            return p;
+        }
+    }
+    if (few) {
+        p.few = true;
+        // Parts: a single wave of CTAs where the items are few (8 x 20000
+        // tokens, 8 kv heads: 116 us in 12 parts, 138 in 47 of 512 tokens); three
+        // waves or more, of at least 384 tokens, where they nearly fill the GPU
+        // and a second wave would be mostly empty (128 x 1200 tokens: 130 us in
+        // one part, 115 in three); else one.
+        const int64_t slots = (int64_t)kPlanSmCount * (head_dim == 128 && block_size == 32 ? 3 : 6);
+        int64_t parts = 1;
+        if (items * 2 <= slots)
+            parts = slots / std::max<int64_t>(1, items);
+        else if (items < 3 * slots)
+            parts = std::max<int64_t>(1, std::min((3 * slots + items - 1) / items, span / 384));
+        const int64_t unit = 64;                // a multiple of either block size
         p.part_tokens = (int)(std::max<int64_t>(1, (span + parts * unit - 1) / (parts * unit)) * unit);
         p.parts = (int)((span + p.part_tokens - 1) / p.part_tokens);
         if (p.parts > 1) {
@@ -1253,25 +1271,9 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
         }
         return p;
     }
-    const int per_tile = pkv::kTreeRows / (num_heads / num_kv_heads);
-    const int row_tiles = (max_query_len + per_tile - 1) / per_tile;
-    p.row_tiles = std::max(1, row_tiles);
-    // Small calls, one wave of CTAs of at most eight key tiles each: clusters of
-    // 1, 2, 4 or 8 CTAs per item.
-    const int64_t tiles = ((int64_t)max_blocks * block_size + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
-    const int64_t items = (int64_t)batch * num_kv_heads * p.row_tiles;
-    if (items <= 2 * kPlanSmCount) {
-        int size = 1;
-        while (size < 8 && items * size * 2 <= 2 * kPlanSmCount && size < tiles)
-            size *= 2;
-        if (tiles <= 8 * size) {
-            p.cluster = size;
-            return p;
-        }
-    }
     p.shares = row_tiles > 1 ? 2 : 1;
     // two CTAs per SM, fewer where the largest such call has less to share out
-    const int64_t units = (int64_t)batch * num_kv_heads * std::max(1, row_tiles) * (tiles + pkv::kTreeItemCost);
+    const int64_t units = items * row_tiles * (tiles + pkv::kTreeItemCost);
     if (units >= (int64_t)1 << 31) {
         p.ctas = 0;             // more than a call's shares are counted in
         return p;
@@ -1355,30 +1357,19 @@ cudaError_t dispatch_tree(int D, int bs, const CUtensorMap &mq, const CacheMaps 
 
 namespace {
 
-// Warps and stages per warp of the few-rows kernel, as for the decode kernel.
-#ifndef PKV_TUNE_NW1
-#define PKV_TUNE_NW1 2
-#define PKV_TUNE_S1 2
-#endif
-#ifndef PKV_TUNE_NW2
-#define PKV_TUNE_NW2 2
-#define PKV_TUNE_S2 2
-#endif
-
-template <int D, int BS, bool BF16, int MT>
+template <int D, int BS, bool BF16>
 cudaError_t launch_tree_rows(const CUtensorMap &mk, const CUtensorMap &mv, const pkv::TreeRowsArgs &a, int batch,
                              cudaStream_t st)
 {
-    constexpr int NW = MT == 1 ? PKV_TUNE_NW1 : PKV_TUNE_NW2, S = MT == 1 ? PKV_TUNE_S1 : PKV_TUNE_S2;
-    constexpr int smem = pkv::TreeRowsShape<D, BS, MT, NW, S>::kSmemBytes;
-    auto kern = pkv::tree_rows_kernel<D, BS, BF16, MT, NW, S>;
+    using Sh = pkv::TreeRowsShape<D, BS>;
+    auto kern = pkv::tree_rows_kernel<D, BS, BF16>;
     static bool configured[64] = {};
     static std::mutex mu;
     const int dev = current_device();
     {
         std::lock_guard<std::mutex> lk(mu);
         if (dev < 0 || dev >= 64 || !configured[dev]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
             if (e != cudaSuccess)
                 return e;
             if (dev >= 0 && dev < 64)
@@ -1386,7 +1377,7 @@ cudaError_t launch_tree_rows(const CUtensorMap &mk, const CUtensorMap &mv, const
         }
     }
     cudaError_t e = launch_pdl(kern, dim3((unsigned)a.num_parts, (unsigned)a.num_kv_heads, (unsigned)batch),
-                               dim3(NW * 32), smem, st, mk, mv, a);
+                               dim3(Sh::kWarps * 32), Sh::kSmemBytes, st, mk, mv, a);
     if (e != cudaSuccess || a.num_parts == 1)
         return e;
     const unsigned eights = (unsigned)((a.max_query_len * a.group + 7) / 8);
@@ -1394,15 +1385,14 @@ cudaError_t launch_tree_rows(const CUtensorMap &mk, const CUtensorMap &mv, const
                       dim3(256), 0, st, a, BS);
 }
 
-template <int D, int BS>
-cudaError_t dispatch_tree_rows(bool bf16, int mt, const CUtensorMap &mk, const CUtensorMap &mv,
+template <bool BF16>
+cudaError_t dispatch_tree_rows(int D, int bs, const CUtensorMap &mk, const CUtensorMap &mv,
                                const pkv::TreeRowsArgs &a, int batch, cudaStream_t st)
 {
-    if (bf16)
-        return mt == 1 ? launch_tree_rows<D, BS, true, 1>(mk, mv, a, batch, st)
-                       : launch_tree_rows<D, BS, true, 2>(mk, mv, a, batch, st);
-    return mt == 1 ? launch_tree_rows<D, BS, false, 1>(mk, mv, a, batch, st)
-                   : launch_tree_rows<D, BS, false, 2>(mk, mv, a, batch, st);
+    if (D == 64 && bs == 16) return launch_tree_rows<64, 16, BF16>(mk, mv, a, batch, st);
+    if (D == 64 && bs == 32) return launch_tree_rows<64, 32, BF16>(mk, mv, a, batch, st);
+    if (D == 128 && bs == 16) return launch_tree_rows<128, 16, BF16>(mk, mv, a, batch, st);
+    return launch_tree_rows<128, 32, BF16>(mk, mv, a, batch, st);
 }
 
 }  // namespace
@@ -1484,12 +1474,9 @@ extern "C" pkv_status pkv_paged_attention_tree(
         f.part_tokens = plan.part_tokens;
         f.num_parts = plan.parts;
         f.scale_log2 = scale_log2;
-        const bool bf = dtype == PKV_BF16;
         const cudaError_t e =
-            head_dim == 64 ? (block_size == 16 ? dispatch_tree_rows<64, 16>(bf, plan.few, mk, mv, f, batch, st)
-                                               : dispatch_tree_rows<64, 32>(bf, plan.few, mk, mv, f, batch, st))
-                           : (block_size == 16 ? dispatch_tree_rows<128, 16>(bf, plan.few, mk, mv, f, batch, st)
-                                               : dispatch_tree_rows<128, 32>(bf, plan.few, mk, mv, f, batch, st));
+            dtype == PKV_BF16 ? dispatch_tree_rows<true>(head_dim, block_size, mk, mv, f, batch, st)
+                              : dispatch_tree_rows<false>(head_dim, block_size, mk, mv, f, batch, st);
         if (e != cudaSuccess)
             return cuda_fail(e, "tree_rows_kernel launch");
         return PKV_OK;

@@ -1343,19 +1343,23 @@ tree_merge_kernel(const TreeArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: up to 32 per (sequence, kv head)
+// Few rows: up to 16 per (sequence, kv head)
 // ---------------------------------------------------------------------------
 // Small trees (or few heads to a group) leave the 128-row tiles above mostly
 // empty, and their calls are bound by the cache's bytes alone.  Here a warp
-// keeps all rows of an item in its own registers and streams pages through a
-// ring of its own, as the decode kernel does: no hand-over between warps, many
-// independent streams per SM.
+// keeps 16 rows in its own registers and streams pages, as the decode kernel
+// does: no hand-over between warps per tile, many independent streams per SM.
 //   S[rows x keys] = Q K^T      mma.sync m16n8k16, Q as A, K rows as B
 //   O[rows x D]   += P V        P straight from S's registers as A, V as B
 // P is split into a 16-bit high part and a 16-bit remainder, each multiplied
-// by V, so the weights keep about 16 bits more.  CTA (part, kv head, sequence)
-// takes part_tokens keys; an item of one part is written out, of several as
-// records that tree_rows_merge_kernel joins.
+// by V, so the weights keep about 16 bits more.  A CTA takes part_tokens keys
+// of a (sequence, kv head), a warp every other page of them.  An item of one
+// part is written out, of several as records that tree_rows_merge_kernel joins.
+// Bound by the cache's bytes: batches of 256 x 576 tokens, 8 kv heads of 128, 2
+// nodes x 4 heads take 110 us (0.89 of the measured copy rate; the 128-row
+// tiles take 132), 40 heads of one node row each more than 1.0 of it.  With 32
+// rows the legacy matrix instructions bound it (174 us against 138), so more
+// rows go to the tiles above.
 struct TreeRowsArgs {
     const uint16_t *query;           // [T, Hq, D]
     const int32_t *query_start;      // [batch + 1]
@@ -1379,51 +1383,39 @@ struct TreeRowsArgs {
     float scale_log2;
 };
 
-template <int D, int BS, int MT, int NW, int S>
+template <int D, int BS>
 struct TreeRowsShape {
-    static constexpr int kRows = MT * 16;
+    static constexpr int kWarps = 2, kStages = 2;            // as the decode kernel
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfBytes = BS * 128;
     static constexpr int kTileBytes = kHalves * kHalfBytes;
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kRingBytes = NW * S * kStageBytes;
-    static constexpr int kMergeBytes = NW * kRows * (D + 2) * 4;
-    static constexpr int kQStride = D * 2 + 16;              // bytes of a Q row: ldmatrix without bank conflicts
-    static constexpr int kQBytes = MT > 1 ? kRows * kQStride : 0;
-    static constexpr int kMain = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-    static constexpr int kSmemBytes = kMain + kQBytes + 1024;
-#ifndef PKV_TUNE_REGS1
-#define PKV_TUNE_REGS1 168
-#endif
-#ifndef PKV_TUNE_REGS2
-#define PKV_TUNE_REGS2 232
-#endif
-    static constexpr int kCtas = 65536 / ((MT == 1 ? PKV_TUNE_REGS1 : PKV_TUNE_REGS2) * NW * 32);
+    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kMergeBytes = kWarps * 16 * (D + 2) * 4;
+    static constexpr int kSmemBytes = (kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes) + 1024;
+    static constexpr int kCtas = 6;                          // per SM, by registers (168)
 };
 
-template <int D, int BS, bool BF16, int MT, int NW, int S>
-__global__ void __launch_bounds__(NW * 32, TreeRowsShape<D, BS, MT, NW, S>::kCtas)
+template <int D, int BS, bool BF16>
+__global__ void __launch_bounds__(TreeRowsShape<D, BS>::kWarps * 32, TreeRowsShape<D, BS>::kCtas)
 tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const TreeRowsArgs a)
 {
-    using Sh = TreeRowsShape<D, BS, MT, NW, S>;
-    constexpr int KS = D / 16, NT = BS / 8, DT = D / 8;
+    using Sh = TreeRowsShape<D, BS>;
+    constexpr int KW = Sh::kWarps, S = Sh::kStages, NT = KW * 32;
+    constexpr int KS = D / 16, NB = BS / 8, DT = D / 8;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[NW * S];
+    __shared__ __align__(8) uint64_t s_full[KW * S];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sq = smem + Sh::kMain;
     const int part = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group;
-    if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            mbar_init(smem_addr(&bars[warp * S + s]), 1);
-    }
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
+    if (threadIdx.x < KW * S)
+        mbar_init(smem_addr(&s_full[threadIdx.x]), 1);
     fence_mbar_init();
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1434,16 +1426,14 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int32_t *trow = a.block_tables + (size_t)b * a.max_blocks + blk0 + warp;
     int ids;
     {
-        const int lb = warp + lane * NW;
-        ids = lb < a.part_tokens / BS && blk0 + lb < a.max_blocks ? __ldg(trow + (size_t)lane * NW) : 0;
+        const int lb = warp + lane * KW;
+        ids = lb < a.part_tokens / BS && blk0 + lb < a.max_blocks ? __ldg(trow + (size_t)lane * KW) : 0;
     }
     TreeSeq s;
-    if (!tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &s)) {
-        if (threadIdx.x == 0 && part == 0 && kvh == 0)
-            raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
-        return;
-    }
-    const int rows = s.n * G;                     // <= kRows
+    const bool good = tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, &s);
+    if (!good && threadIdx.x == 0 && part == 0 && kvh == 0)
+        raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
+    const int rows = s.n * G;                     // <= 16 (0 for a sequence that contradicts itself)
     const int tok0 = part * a.part_tokens;
     const int tok1 = min(s.len, tok0 + a.part_tokens);
     if (rows == 0 || tok1 <= tok0)
@@ -1451,14 +1441,14 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const bool split = s.len > a.part_tokens;
     const int base = s.len - s.n;
     const int nblk = (tok1 - tok0 + BS - 1) / BS;
-    const int nk = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;   // this warp's blocks
+    const int nk = nblk > warp ? (nblk - warp + KW - 1) / KW : 0;   // this warp's blocks
     uint8_t *ring = smem + (size_t)warp * S * Sh::kStageBytes;
     const uint32_t ring_s = smem_addr(ring);
-    const uint32_t bar0 = smem_addr(&bars[warp * S]);
+    const uint32_t full0 = smem_addr(&s_full[warp * S]);
     const uint64_t policy = policy_evict_first();
     auto issue = [&](int k) {
         if ((k & 31) == 0 && k > 0)
-            ids = k + lane < nk ? __ldg(trow + (size_t)(k + lane) * NW) : 0;
+            ids = k + lane < nk ? __ldg(trow + (size_t)(k + lane) * KW) : 0;
         int blk = __shfl_sync(0xffffffffu, ids, k & 31);
         if ((unsigned)blk >= (unsigned)a.num_blocks) {
             if (lane == 0)
@@ -1466,7 +1456,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             blk = 0;
         }
         if (lane == 0) {
-            const uint32_t bar = bar0 + 8u * (k % S);
+            const uint32_t bar = full0 + 8u * (k % S);
             const uint32_t dk = ring_s + (uint32_t)((k % S) * Sh::kStageBytes), dv = dk + Sh::kTileBytes;
             mbar_arrive_expect_tx(bar, Sh::kStageBytes);
 #pragma unroll
@@ -1476,61 +1466,38 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
         }
     };
-    const int pre = nk < S ? nk : S;
-    for (int k = 0; k < pre; ++k)
-        issue(k);
+    int issued = 0, consumed = 0;
+    for (; issued < (nk < S ? nk : S); ++issued)
+        issue(issued);
 
-    // ---- Q: one 16-row tile in registers, two in shared memory ----
-    // row r is (node r / G, head r % G)
+    // ---- Q fragments: row r of the item is (node r / G, head r % G) ----
     const int g0 = lane >> 2, c2 = (lane & 3) * 2;
+    const int ra = g0, rb = g0 + 8;               // this lane's rows
     auto q_row = [&](int r) {
-        return a.query + ((size_t)(s.q0 + r / G) * a.num_heads + (size_t)kvh * G + r % G) * D;
+        r = r < rows ? r : 0;
+        return reinterpret_cast<const uint32_t *>(
+            a.query + ((size_t)(s.q0 + r / G) * a.num_heads + (size_t)kvh * G + r % G) * D + c2);
     };
-    uint32_t qf[MT > 1 ? 1 : KS][4];
-    if constexpr (MT == 1) {
-        const uint32_t *q0 = reinterpret_cast<const uint32_t *>(q_row(g0 < rows ? g0 : 0) + c2);
-        const uint32_t *q1 = reinterpret_cast<const uint32_t *>(q_row(g0 + 8 < rows ? g0 + 8 : 0) + c2);
+    uint32_t qf[KS][4];
+    {
+        const uint32_t *qa = q_row(ra), *qb = q_row(rb);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            qf[ks][0] = __ldg(q0 + ks * 8);
-            qf[ks][1] = __ldg(q1 + ks * 8);
-            qf[ks][2] = __ldg(q0 + ks * 8 + 4);
-            qf[ks][3] = __ldg(q1 + ks * 8 + 4);
+            qf[ks][0] = __ldg(qa + ks * 8);
+            qf[ks][1] = __ldg(qb + ks * 8);
+            qf[ks][2] = __ldg(qa + ks * 8 + 4);
+            qf[ks][3] = __ldg(qb + ks * 8 + 4);
         }
-    } else {
-        for (int i = threadIdx.x; i < Sh::kRows * (D / 8); i += NW * 32) {
-            const int r = i / (D / 8), v = i % (D / 8);
-            *reinterpret_cast<uint4 *>(sq + r * Sh::kQStride + v * 16) =
-                r < rows ? __ldg(reinterpret_cast<const uint4 *>(q_row(r)) + v) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        __syncthreads();
     }
-    const uint32_t sq_s = smem_addr(sq) + (uint32_t)((lane & 15) * Sh::kQStride + (lane >> 4) * 16);
-    // this lane's rows' nodes, for their mask rows
-    int node[MT][2];
+    float m_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f}, acc[DT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = mt * 16 + h * 8 + g0;
-            node[mt][h] = r < rows ? r / G : 0;
-        }
-
-    float m_run[MT][2], l_run[MT][2], acc[MT][DT][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        m_run[mt][0] = m_run[mt][1] = kNegInf;
-        l_run[mt][0] = l_run[mt][1] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[mt][d][i] = 0.f;
-    }
-    int issued = pre, consumed = 0;
+        for (int i = 0; i < 4; ++i)
+            acc[d][i] = 0.f;
     for (int k = 0; k < nk; ++k) {
         const int st = k % S;
-        const bool got = mbar_wait_bounded(bar0 + 8u * st, (uint32_t)((k / S) & 1), kWaitLimitNs);
+        const bool got = mbar_wait_bounded(full0 + 8u * st, (uint32_t)((k / S) & 1), kWaitLimitNs);
         if (!__all_sync(0xffffffffu, got)) {
             if (lane == 0)
                 raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
@@ -1538,13 +1505,13 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         consumed = k + 1;
         const uint32_t sk = ring_s + (uint32_t)(st * Sh::kStageBytes), sv = sk + Sh::kTileBytes;
-        const int p0 = (blk0 + warp + k * NW) * BS;      // the block's first position
+        const int p0 = (blk0 + warp + k * KW) * BS;        // the block's first position
         const bool masked = p0 + BS > base;
         bool bad = false;
         if (masked) {
-            // cells past the end may hold anything: zero; infinities and NaN
+            // Cells past the end may hold anything: zero.  Infinities and NaN
             // of drafted cells are zeroed too and added below to the rows that
-            // see them (weight 0 times such a value would not be 0)
+            // see them (weight 0 times such a value would not be 0).
             uint8_t *vt = ring + (size_t)st * Sh::kStageBytes + Sh::kTileBytes;
             const int valid = min(BS, s.len - p0);
             uint32_t any = 0u;
@@ -1572,121 +1539,95 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             __syncwarp();
         }
         // ---- scores ----
-        float sc[MT][NT][4];
+        float sc[NB][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int i = 0; i < 4; ++i)
+                sc[j][i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc[mt][j][i] = 0.f;
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint32_t qa[MT][4];
-            if constexpr (MT == 1) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qa[0][i] = qf[ks][i];
-            } else {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    ldsm_x4(sq_s + (uint32_t)(mt * 16 * Sh::kQStride + ks * 32), qa[mt]);
-            }
-#pragma unroll
-            for (int j = 0; j < NT; j += 2) {
+            for (int j = 0; j < NB; j += 2) {
                 const int key = j * 8 + (lane >> 4) * 8 + (lane & 7);
                 const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
                 uint32_t kf[4];
                 ldsm_x4(sk + (uint32_t)((ks >> 2) * Sh::kHalfBytes + key * 128 + ((chunk ^ (key & 7)) << 4)), kf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma_16816<BF16>(sc[mt][j], qa[mt], kf[0], kf[1]);
-                    mma_16816<BF16>(sc[mt][j + 1], qa[mt], kf[2], kf[3]);
-                }
+                mma_16816<BF16>(sc[j], qf[ks], kf[0], kf[1]);
+                mma_16816<BF16>(sc[j + 1], qf[ks], kf[2], kf[3]);
             }
-        }
         // ---- mask, online softmax (base 2) ----
-        uint32_t vis[MT][2];
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+        float alpha[2];
         bool any_resc = false;
-        float alpha[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                vis[mt][h] = 0xffffffffu;
-                if (masked) {
-                    const int32_t *mrow = a.tree_mask + (size_t)(s.q0 + node[mt][h]) * a.words;
-                    vis[mt][h] = (uint32_t)tree_bits(mrow, a.words, base, s.n, p0);
-                }
-                float mx = kNegInf;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &x = sc[mt][j][2 * h + i];
-                        x *= a.scale_log2;
-                        if (masked)
-                            x = (vis[mt][h] >> (j * 8 + c2 + i)) & 1u ? x : kNegInf;
-                        mx = fmaxf(mx, x);
-                    }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // the running maximum moves when a block exceeds it by 2^8
-                const bool move = mx > m_run[mt][h] + 8.f;
-                const float mnew = move ? mx : m_run[mt][h];
-                alpha[mt][h] = move ? ex2(m_run[mt][h] - mnew) : 1.f;
-                any_resc |= move;
-                m_run[mt][h] = mnew;
-                const float msub = mnew == kNegInf ? 0.f : mnew;
-                float ls = 0.f;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &x = sc[mt][j][2 * h + i];
-                        x = ex2(x - msub);
-                        ls += x;
-                    }
-                l_run[mt][h] = l_run[mt][h] * alpha[mt][h] + ls;
+        for (int h = 0; h < 2; ++h) {
+            if (masked) {
+                const int r = h ? rb : ra;
+                vis[h] = (uint32_t)tree_bits(a.tree_mask + (size_t)(s.q0 + (r < rows ? r / G : 0)) * a.words, a.words,
+                                             base, s.n, p0);
             }
+            float mx = kNegInf;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float &x = sc[j][2 * h + i];
+                    x *= a.scale_log2;
+                    if (masked)
+                        x = (vis[h] >> (j * 8 + c2 + i)) & 1u ? x : kNegInf;
+                    mx = fmaxf(mx, x);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // the running maximum moves when a block exceeds it by 2^8
+            const bool move = mx > m_run[h] + 8.f;
+            const float mnew = move ? mx : m_run[h];
+            alpha[h] = move ? ex2(m_run[h] - mnew) : 1.f;
+            any_resc |= move;
+            m_run[h] = mnew;
+            const float msub = mnew == kNegInf ? 0.f : mnew;
+            float ls = 0.f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float &x = sc[j][2 * h + i];
+                    x = ex2(x - msub);
+                    ls += x;
+                }
+            l_run[h] = l_run[h] * alpha[h] + ls;
         }
         if (__any_sync(0xffffffffu, any_resc)) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    acc[mt][d][0] *= alpha[mt][0];
-                    acc[mt][d][1] *= alpha[mt][0];
-                    acc[mt][d][2] *= alpha[mt][1];
-                    acc[mt][d][3] *= alpha[mt][1];
-                }
+            for (int d = 0; d < DT; ++d) {
+                acc[d][0] *= alpha[0];
+                acc[d][1] *= alpha[0];
+                acc[d][2] *= alpha[1];
+                acc[d][3] *= alpha[1];
+            }
         }
         // ---- O += P V, 16 keys at a time ----
 #pragma unroll
         for (int kb = 0; kb < BS / 16; ++kb) {
-            uint32_t ph[MT][4], pl[MT][4];
+            uint32_t ph[4], pl[4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float *x = &sc[mt][2 * kb + (i >> 1)][2 * (i & 1)];
-                    ph[mt][i] = pack2<BF16>(x[0], x[1]);
-                    const float2 f = unpack2<BF16>(ph[mt][i]);
-                    pl[mt][i] = pack2<BF16>(x[0] - f.x, x[1] - f.y);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float *x = &sc[2 * kb + (i >> 1)][2 * (i & 1)];
+                ph[i] = pack2<BF16>(x[0], x[1]);
+                const float2 f = unpack2<BF16>(ph[i]);
+                pl[i] = pack2<BF16>(x[0] - f.x, x[1] - f.y);
+            }
             const int key = kb * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int d = 0; d < DT; d += 2) {
                 const int chunk = (d & 7) + (lane >> 4);
                 uint32_t vf[4];
                 ldsm_x4_trans(sv + (uint32_t)((d >> 3) * Sh::kHalfBytes + key * 128 + ((chunk ^ (key & 7)) << 4)), vf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma_16816<BF16>(acc[mt][d], ph[mt], vf[0], vf[1]);
-                    mma_16816<BF16>(acc[mt][d + 1], ph[mt], vf[2], vf[3]);
-                    mma_16816<BF16>(acc[mt][d], pl[mt], vf[0], vf[1]);
-                    mma_16816<BF16>(acc[mt][d + 1], pl[mt], vf[2], vf[3]);
-                }
+                mma_16816<BF16>(acc[d], ph, vf[0], vf[1]);
+                mma_16816<BF16>(acc[d + 1], ph, vf[2], vf[3]);
+                mma_16816<BF16>(acc[d], pl, vf[0], vf[1]);
+                mma_16816<BF16>(acc[d + 1], pl, vf[2], vf[3]);
             }
         }
         if (bad) {
@@ -1702,15 +1643,13 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     const uint32_t f = nonfinite2<BF16>(x);
                     const float2 y = unpack2<BF16>(x);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if ((vis[mt][h] >> c) & 1u) {
-                                if (f & 1u)
-                                    acc[mt][d][2 * h] += y.x;
-                                if (f >> 16)
-                                    acc[mt][d][2 * h + 1] += y.y;
-                            }
+                    for (int h = 0; h < 2; ++h)
+                        if ((vis[h] >> c) & 1u) {
+                            if (f & 1u)
+                                acc[d][2 * h] += y.x;
+                            if (f >> 16)
+                                acc[d][2 * h + 1] += y.y;
+                        }
                 }
             }
         }
@@ -1722,43 +1661,39 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     // a wait gave up: copies in flight land (bounded) before the memory is reused
     for (int k = consumed; k < issued; ++k)
-        mbar_wait_bounded(bar0 + 8u * (k % S), (uint32_t)((k / S) & 1), kWaitLimitNs / 8);
+        mbar_wait_bounded(full0 + 8u * (k % S), (uint32_t)((k / S) & 1), kWaitLimitNs / 8);
 
     // ---- merge the warps by log-sum-exp through shared memory ----
     __syncthreads();
-    float *so = reinterpret_cast<float *>(smem);         // [NW][kRows][D]
-    float2 *sml = reinterpret_cast<float2 *>(so + NW * Sh::kRows * D);   // [NW][kRows]
+    float *so = reinterpret_cast<float *>(smem);                      // [warps][16][D]
+    float2 *sml = reinterpret_cast<float2 *>(so + KW * 16 * D);   // [warps][16]
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + g0;
+        float l = l_run[h];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if ((lane & 3) == 0)
+            sml[warp * 16 + r] = make_float2(m_run[h], l);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = mt * 16 + h * 8 + g0;
-            float l = l_run[mt][h];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if ((lane & 3) == 0)
-                sml[warp * Sh::kRows + r] = make_float2(m_run[mt][h], l);
-            if (r < rows) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    *reinterpret_cast<float2 *>(so + (warp * Sh::kRows + r) * D + d * 8 + c2) =
-                        make_float2(acc[mt][d][2 * h], acc[mt][d][2 * h + 1]);
-            }
-        }
+        for (int d = 0; d < DT; ++d)
+            *reinterpret_cast<float2 *>(so + (warp * 16 + r) * D + d * 8 + c2) =
+                make_float2(acc[d][2 * h], acc[d][2 * h + 1]);
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += NW * 32) {
+    for (int i = threadIdx.x; i < rows * (D / 4); i += NT) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         float M = kNegInf;
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-            M = fmaxf(M, sml[w * Sh::kRows + r].x);
+        for (int w = 0; w < KW; ++w)
+            M = fmaxf(M, sml[w * 16 + r].x);
         float den = 0.f;
         float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float2 ml = sml[w * Sh::kRows + r];
+        for (int w = 0; w < KW; ++w) {
+            const float2 ml = sml[w * 16 + r];
             const float e = ml.x == kNegInf ? 1.f : ex2(ml.x - M);   // (1: no keys seen, or all NaN)
-            const float4 o = *reinterpret_cast<const float4 *>(so + (w * Sh::kRows + r) * D + d);
+            const float4 o = *reinterpret_cast<const float4 *>(so + (w * 16 + r) * D + d);
             den += e * ml.y;
             num.x += e * o.x;
             num.y += e * o.y;
