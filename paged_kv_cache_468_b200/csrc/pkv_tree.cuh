@@ -881,9 +881,10 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             constexpr uint32_t idO = f16_idesc<BF16>(kTreeRows, D, true);
             int ks_ = 0, kround = 0;                 // K stage of the next S
             // S of global tile J; u: its part (Q buffer); last: the part's last S
-            auto issue_s = [&](int J, int u, bool last) -> bool {
-                if (!mbar_wait_bounded(bar(Sh::kKFull + ks_), (uint32_t)(kround & 1), kWaitLimitNs))
-                    return false;
+            auto k_ready = [&]() -> bool {
+                return mbar_wait_bounded(bar(Sh::kKFull + ks_), (uint32_t)(kround & 1), kWaitLimitNs);
+            };
+            auto issue_s = [&](int J, int u, bool last) {
                 tc_fence_after();
                 const uint32_t kt = sK + ks_ * Sh::kKVBytes;
                 // with two Q buffers the rows past a buffer's 64 read what lies
@@ -903,7 +904,6 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ks_ = 0;
                     ++kround;
                 }
-                return true;
             };
             auto q_ready = [&](int u) -> bool {
                 return mbar_wait_bounded(bar(Sh::kQFull + (two_q ? u & 1 : 0)), (uint32_t)((two_q ? u >> 1 : u) & 1),
@@ -914,8 +914,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             bool ok = true;
             int J = 0, u = 0, vs = 0, vround = 0;
             int scans = 0;
-            if (has)
-                ok = q_ready(0) && issue_s(0, 0, s.k1 - s.k0 == 1);
+            if (has && (ok = q_ready(0) && k_ready()))
+                issue_s(0, 0, s.k1 - s.k0 == 1);
             while (ok && has) {
                 const int cnt = s.k1 - s.k0;
                 const int first_masked = (s.len - s.n) / kTreeKeys - s.k0;   // (tiles of this part)
@@ -925,18 +925,20 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // tile's P V: it overwrites the buffer that P_{J-1} V_{J-1}
                     // reads.  With one Q buffer the next part's first S comes
                     // after P V: its Q may still be on the way.
-                    if (!last || (has_nx && two_q)) {
-                        if (J >= 1 && !(ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs)))
-                            break;
-                        ok = last ? q_ready(u + 1) && issue_s(J + 1, u + 1, nx.k1 - nx.k0 == 1)
-                                  : issue_s(J + 1, u, j + 2 == cnt);
-                        if (!ok)
-                            break;
-                    }
-                    // a masked tile's V rows are scanned (warp 7) while the softmax works
+                    const bool ahead = !last || (has_nx && two_q);
+                    // what has landed long since is looked at first: each look
+                    // costs 100-200 cycles, and P_{J-1} V_{J-1} runs meanwhile
                     ok = mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs);
-                    if (ok && j >= first_masked) {
-                        mbar_arrive(bar(Sh::kScanReq));
+                    const bool scan = j >= first_masked;
+                    if (ok && scan)
+                        mbar_arrive(bar(Sh::kScanReq));      // warp 7 scans V while the softmax works
+                    if (ok && ahead) {
+                        ok = (!last || q_ready(u + 1)) && k_ready() &&
+                             (J == 0 || mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs));
+                        if (ok)
+                            issue_s(J + 1, last ? u + 1 : u, last ? nx.k1 - nx.k0 == 1 : j + 2 == cnt);
+                    }
+                    if (ok && scan) {
                         ok = mbar_wait_bounded(bar(Sh::kScanned), (uint32_t)(scans & 1), kWaitLimitNs);
                         ++scans;
                     }
@@ -959,9 +961,10 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (last && has_nx && !two_q) {
                         // O_DONE of this tile: it completes after the MMAs that read
                         // the buffer, and a wait for the phase before could miss it
-                        if (!(ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)(J & 1), kWaitLimitNs) && q_ready(u + 1) &&
-                                   issue_s(J + 1, u + 1, nx.k1 - nx.k0 == 1)))
+                        if (!(ok = q_ready(u + 1) && k_ready() &&
+                                   mbar_wait_bounded(bar(Sh::kODone), (uint32_t)(J & 1), kWaitLimitNs)))
                             break;
+                        issue_s(J + 1, u + 1, nx.k1 - nx.k0 == 1);
                     }
                 }
                 if (!ok)
