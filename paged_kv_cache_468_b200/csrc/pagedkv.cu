@@ -1233,7 +1233,9 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
     const int64_t span = (int64_t)max_blocks * block_size;
     const int64_t tiles = (span + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
     const int64_t items = (int64_t)batch * num_kv_heads;
-    const bool few = max_query_len * group <= 16;
+    // (pages of 32 x 128 leave room for three few-rows CTAs per SM only: over
+    // long contexts the tiles are ahead, 140 us against 154 for 8 x 16-32 K tokens)
+    const bool few = max_query_len * group <= 16 && !(head_dim == 128 && block_size == 32 && span >= 4096);
     p.row_tiles = row_tiles;
     // Small calls, one wave of CTAs of at most eight key tiles each: clusters of
     // 1, 2, 4 or 8 CTAs per item (8 sequences of 600 tokens, 4 nodes of 32/8

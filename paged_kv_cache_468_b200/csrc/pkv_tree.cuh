@@ -529,10 +529,6 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tensormap(&tm_v4);
     }
     fence_mbar_init();
-    if (warp == 5) {
-        tmem_alloc(smem_addr(&loc->tmem), kTmemCols);
-        tmem_relinquish();
-    }
     // masked columns of a tile may meet V rows that no load has filled
     {
         uint4 *vr = reinterpret_cast<uint4 *>(data + Sh::kVOff);
@@ -542,6 +538,11 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    // (after the wait: a kernel before this one may still be taking its own)
+    if (warp == 5) {
+        tmem_alloc(smem_addr(&loc->tmem), kTmemCols);
+        tmem_relinquish();
+    }
 
     int cl_tiles = 0, cl_rows = 0, cl_q0 = 0, cl_kvh = 0;   // CL: the item, if it is joined (else cl_rows is 0)
     if constexpr (CL) {

@@ -8,6 +8,7 @@ fallback: if the library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import Optional
@@ -406,6 +407,9 @@ def paged_attention_decode_cascade(query: torch.Tensor, key_cache: torch.Tensor,
 
 
 # ---- speculative decoding with drafted token trees ----
+_KIND = operator.attrgetter("dtype", "shape", "device")
+
+
 # These calls run many times per generated token, so the checks below are kept
 # to a few attribute reads per tensor.
 def _tensor(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
@@ -581,11 +585,14 @@ def kv_cache_compact(key_caches, value_caches, block_tables: torch.Tensor, start
     if block_tables.dim() != 2 or keep.dim() != 2:
         raise ValueError("block_tables must be int32 [batch, max_blocks], keep int32 [batch, max_keep]")
     (B, MB), K = block_tables.shape, keep.shape[1]
-    ptrs, dtype = [], first.dtype
-    for c in (*key_caches, *value_caches):
-        if c.dtype is not dtype or c.shape != shape or c.device != dev or not c.is_contiguous():
-            raise ValueError("the caches must share one shape, element type and device, and be contiguous")
-        ptrs.append(c.data_ptr())
+    caches = [*key_caches, *value_caches]
+    want = (first.dtype, shape, dev)
+    for kind in map(_KIND, caches):
+        if kind != want:
+            raise ValueError("the caches must share one shape, element type and device")
+    if not all(map(torch.Tensor.is_contiguous, caches)):
+        raise ValueError("the caches must be contiguous")
+    ptrs = list(map(torch.Tensor.data_ptr, caches))
     if len(set(ptrs)) != 2 * N:
         raise ValueError("the caches of a call must all be different tensors")
     args = (_tensor(block_tables, "block_tables", torch.int32, (B, MB), dev), MB,

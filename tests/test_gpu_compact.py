@@ -146,3 +146,34 @@ def test_repeats_in_a_graph_on_a_stream_and_with_a_workspace():
         torch.cuda.synchronize()
         way()
         assert same()
+
+
+def test_large_batch_and_two_graphs_with_one_workspace():
+    g = torch.Generator().manual_seed(12)
+    spans = [int(x) for x in torch.randint(0, 300, (900,), generator=g)]
+    kept = [int(torch.randint(0, s + 1, (1,), generator=g)) for s in spans]
+    starts = [int(x) for x in torch.randint(0, 40, (900,), generator=g)]
+    cases = [_case(spans, kept, starts, 1, 1, 32, 16, seed=13), _case([2000, 700], [900, 699], [3, 0], 2, 2, 64, 16, seed=14)]
+    need = max(pkv.compact_workspace_bytes(c["layers"], len(c["lists"]), c["keep"].shape[1], c["caches"][0].shape[2],
+                                           c["caches"][0].shape[3]) for c in cases)
+    ws = torch.full((need,), 255, dtype=torch.uint8).cuda()
+    graphs, held = [], []
+    for c in cases:
+        d = [x.cuda() for x in c["caches"]]
+        n = c["layers"]
+        args = (d[:n], d[n:], c["table"].cuda(), c["starts"].cuda(), c["keep"].cuda(), c["lens"].cuda())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pkv.kv_cache_compact(*args, workspace=ws)
+        held.append((d, args))
+    for gr in graphs:
+        gr.replay()
+    torch.cuda.synchronize()
+    for c, (d, _) in zip(cases, held):
+        _check(c, d)
+
+
+@pytest.mark.parametrize("K", [16, 17, 256, 257])
+def test_list_lengths_where_the_kernel_changes(K):
+    c = _case([3 * K, K, K + 1], [K, K, K], [0, 20, 7], 2, 3, 40, 16, seed=K)
+    _check(c, _run(c))

@@ -285,6 +285,122 @@ def test_attend_repeats_bit_for_bit_and_in_a_graph_and_on_a_stream():
     assert torch.equal(held, first)
 
 
+# A wide table makes the library plan for long contexts: equal shares of key
+# tiles per CTA (over 16 rows), parts of a context (up to 16), instead of
+# clusters.  The same contexts then run through the other kernels.
+_WIDE = {16: 4096, 32: 2048}
+
+
+@pytest.mark.parametrize("Hq,Hkv,nodes", [(8, 2, [5, 0, 1, 33, 17, 2]), (3, 1, [50, 1, 90]), (8, 1, [300, 3, 150]),
+                                          (4, 2, [2, 8, 1, 0, 5]), (1, 1, [16, 3, 9]), (7, 1, [2, 1])])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 32), (128, 16), (64, 32)])
+def test_attend_planned_for_long_contexts(Hq, Hkv, nodes, D, bs):
+    bases = [40, 100, 0, 63, 1300, 1][:len(nodes)]
+    c = tu.tree_case(nodes, bases, Hq, Hkv, D, bs, "bf16" if D == 64 else "f16", seed=D + bs + Hq, columns=_WIDE[bs])
+    d = _cuda(c)
+    out = _attend(d)
+    _check(c, out)
+    for _ in range(5):
+        assert torch.equal(_attend(d), out)
+
+
+@pytest.mark.parametrize("n,base", [(1, 0), (1, 63), (20, 0), (33, 31), (16, 48), (16, 49), (65, 0), (129, 31), (31, 33)])
+def test_attend_borders_planned_for_long_contexts(n, base):
+    c = tu.tree_case([n], [base], 4, 1, 128, 16, "f16", seed=n * 1000 + base, columns=_WIDE[16])
+    _check(c, _attend(_cuda(c)))
+
+
+def test_attend_any_bits_planned_for_long_contexts():
+    g = torch.Generator().manual_seed(25)
+    nodes, bases = [40, 6, 70, 3], [0, 0, 100, 20]
+    bits = [(torch.rand(n, 96, generator=g) < 0.3).numpy() for n in nodes]
+    for x, n in zip(bits, nodes):
+        x[n // 2] = False
+        x[n // 2, n:] = True
+    c = tu.tree_case(nodes, bases, 4, 2, 64, 16, "bf16", seed=26, bits=bits, max_query_len=96, columns=_WIDE[16])
+    out = _attend(_cuda(c))
+    _check(c, out)
+    assert (out[20] == 0).all() and (out[43] == 0).all()
+
+
+@pytest.mark.parametrize("heads", [(4, 2), (16, 2)])
+@pytest.mark.parametrize("columns", [0, 4096])
+def test_attend_nonfinite_cells_in_every_kernel(heads, columns):
+    parents = torch.tensor([-1, 0, 0, 1, 1, 3, 2], dtype=torch.int32)
+    bits = tu.ancestors(parents)[0]
+    nodes, bases = [7, 7, 7], [200, 0, 57]
+    c = tu.tree_case(nodes, bases, *heads, 128, 16, "f16", seed=28, bits=[bits] * 3, columns=columns)
+    for b, base in enumerate(bases):
+        page, cell = int(c["block_tables"][b, (base + 3) // 16]), (base + 3) % 16
+        c["value_cache"][page, cell, :, 70] = float("inf")
+        c["value_cache"][page, cell, :, 6] = float("nan")
+        c["key_cache"][page, cell, :, 9] = float("nan") if b == 2 else c["key_cache"][page, cell, :, 9]
+        c["values"][b][base + 3] = 0.0
+    out = _attend(_cuda(c)).cpu()
+    ref, tol = tu.attend_reference(c)
+    blind = [7 * b + i for b in range(3) for i in (0, 1, 2, 4, 6)]
+    assert ((out.double() - ref).abs() <= tol)[blind].all()
+    for b in range(3):
+        for i in (3, 5):
+            row = out[7 * b + i]
+            if b == 2:
+                assert row.isnan().all()                   # a NaN score
+            else:
+                assert (row[:, 70] == float("inf")).all() and row[:, 6].isnan().all()
+                assert row[:, :6].isfinite().all() and row[:, 7:70].isfinite().all() and row[:, 71:].isfinite().all()
+
+
+def test_attend_many_short_sequences():
+    # more sequences than a CTA has threads, some without rows; shares hold many small items
+    g = torch.Generator().manual_seed(27)
+    nodes = [int(x) for x in torch.randint(0, 9, (700,), generator=g)]
+    bases = [int(x) for x in torch.randint(0, 40, (700,), generator=g)]
+    for heads, columns in (((4, 1), 0), ((4, 1), 600), ((1, 1), 0)):
+        c = tu.tree_case(nodes, bases, *heads, 64, 16, "bf16", seed=29, columns=columns)
+        _check(c, _attend(_cuda(c)))
+
+
+def test_attend_largest_tree():
+    c = tu.tree_case([1024, 700], [17, 64], 2, 1, 64, 16, "bf16", seed=30)
+    _check(c, _attend(_cuda(c)))
+    c = tu.tree_case([1024], [30], 1, 1, 128, 32, "f16", seed=31, columns=4096)
+    _check(c, _attend(_cuda(c)))
+
+
+def test_attend_negative_zero_and_tiny_scale():
+    for scale in (-0.3, 0.0, 1e-6):
+        c = tu.tree_case([20, 5], [90, 0], 4, 2, 64, 16, "bf16", seed=32)
+        c["scale"] = scale
+        _check(c, _attend(_cuda(c)))
+        c = tu.tree_case([3, 5], [90, 0], 2, 2, 64, 16, "bf16", seed=33)
+        c["scale"] = scale
+        _check(c, _attend(_cuda(c)))
+
+
+def test_two_graphs_share_a_workspace_and_two_streams_have_their_own():
+    cases = [tu.tree_case([30] * 6, [100 * i for i in range(6)], 4, 2, 64, 16, "bf16", seed=40 + k, columns=4096) for k in range(2)]
+    ds = [_cuda(c) for c in cases]
+    need = pkv.tree_workspace_bytes(6, 30, 180, 4, 2, 64, 4096, 16)
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8).cuda()
+    want = [_attend(d) for d in ds]
+    graphs, held = [], []
+    for d in ds:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(_attend(d, workspace=ws))
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held, want))
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    got = [[_attend(d, stream=s) for d, s in zip(ds, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for outs in got for a, b in zip(outs, want))
+
+
 # ---- a whole step ----
 def test_verification_step_end_to_end():
     """Draft, write, mask, attend, accept, compact, truncate; then a decode over what is left equals

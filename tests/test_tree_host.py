@@ -64,12 +64,16 @@ def test_tree_attention_host_validation():
     assert call(mask=A16 + 2) == pagedkv.ERR_MISALIGNED
     assert call(B=0, q=None, out=None) == pagedkv.OK
     assert call(T=0, q=None, out=None) == pagedkv.OK
-    need = pkv.tree_workspace_bytes(2, 32, 64, 8, 2, 128, 8, 16)
+    assert pkv.tree_workspace_bytes(2, 32, 64, 8, 2, 128, 8, 16) == 0      # a small call: no workspace
+    need = pkv.tree_workspace_bytes(2, 32, 64, 8, 2, 128, 4096, 16)
     assert need > 0
-    if need:
-        assert call(ws=None) == pagedkv.ERR_WORKSPACE
-        assert call(wsb=need - 1) == pagedkv.ERR_WORKSPACE
-        assert call(ws=A16 + 8) == pagedkv.ERR_MISALIGNED
+    assert call(mb=4096, ws=None) == pagedkv.ERR_WORKSPACE
+    assert call(mb=4096, wsb=need - 1) == pagedkv.ERR_WORKSPACE
+    assert call(mb=4096, ws=A16 + 8) == pagedkv.ERR_MISALIGNED
+    assert pkv.tree_workspace_bytes(2, 32, 64, 8, 2, 96, 4096, 16) == 0    # a shape that the call refuses
+    # more units than a call counts: 60000 sequences x 8 kv heads x 32 row tiles x 256 key tiles
+    assert pkv.tree_workspace_bytes(60000, 512, 64, 64, 8, 128, 1024, 16) == 0
+    assert call(B=60000, T=1 << 20, mql=512, Hq=64, Hkv=8, mb=1024) == pagedkv.ERR_UNSUPPORTED
 
 
 def test_compact_host_validation():
@@ -95,9 +99,12 @@ def test_compact_host_validation():
     assert call(n=0, caches=None) == pagedkv.OK
     assert call(B=0, bt=None) == pagedkv.OK
     assert call(K=0, kp=None) == pagedkv.OK
-    if pkv.compact_workspace_bytes(2, 2, 500, 2, 64):
-        assert call(ws=None) == pagedkv.ERR_WORKSPACE
-        assert call(wsb=1) == pagedkv.ERR_WORKSPACE
+    need = pkv.compact_workspace_bytes(2, 2, 500, 2, 64)
+    assert need > 0 and pkv.compact_workspace_bytes(2, 2, 100, 2, 64) == 0
+    assert call(ws=None) == pagedkv.ERR_WORKSPACE
+    assert call(wsb=need - 1) == pagedkv.ERR_WORKSPACE
+    assert call(ws=A16 + 2) == pagedkv.ERR_MISALIGNED
+    assert call(K=(1 << 30) - 1, mb=1 << 25, B=60000) == pagedkv.ERR_UNSUPPORTED   # chunks past 2^31
 
 
 def test_binding_refuses_wrong_tensors():

@@ -55,16 +55,17 @@ def accept(parents, draft, target):
         path.append(following[0])
 
 
-def tree_case(nodes, bases, Hq, Hkv, D, bs, dtype, seed, bits=None, q_scale=1.0, max_query_len=None):
+def tree_case(nodes, bases, Hq, Hkv, D, bs, dtype, seed, bits=None, q_scale=1.0, max_query_len=None, columns=0):
     """Drafted trees of `nodes[b]` nodes behind `bases[b]` committed tokens.  bits[b]: [n, n] truth
-    values (default: a random tree's ancestors).  Cells that belong to no token hold NaN."""
+    values (default: a random tree's ancestors).  Cells that belong to no token hold NaN.  columns: the
+    table's width at least (a wide table makes the library plan for long contexts)."""
     g = torch.Generator().manual_seed(seed)
     B = len(nodes)
     lens = [n + c for n, c in zip(nodes, bases)]
     pages = [-(-t // bs) for t in lens]
     NB = sum(pages) + 5
     order = torch.randperm(NB, generator=g).tolist()
-    table = torch.full((B, max(1, max(pages))), -1, dtype=torch.int32)
+    table = torch.full((B, max(1, columns, max(pages))), -1, dtype=torch.int32)
     kc = torch.full((NB, bs, Hkv, D), float("nan"))
     vc = torch.full((NB, bs, Hkv, D), float("nan"))
     ks, vs = [], []
