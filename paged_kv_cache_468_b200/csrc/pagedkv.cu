@@ -1217,6 +1217,7 @@ namespace {
 // CTAs of a tree attention call and the layout of its records.
 struct TreePlan {
     bool few;                   // the few-rows kernel
+    bool transposed;            // keys as the products' rows
     int part_tokens, parts;     // few rows: keys of a part, parts of the longest item
     int cluster;                // 128-row tiles: CTAs per item of a small call, 0: shares
     int row_tiles;
@@ -1231,10 +1232,10 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
     const int per_tile = pkv::kTreeRows / group;
     const int row_tiles = std::max(1, (max_query_len + per_tile - 1) / per_tile);
     const int64_t span = (int64_t)max_blocks * block_size;
-    const int64_t tiles = (span + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
+    int64_t tiles = (span + pkv::kTreeKeys - 1) / pkv::kTreeKeys;
     const int64_t items = (int64_t)batch * num_kv_heads;
     // (pages of 32 x 128 leave room for three few-rows CTAs per SM only: over
-    // long contexts the tiles are ahead, 140 us against 154 for 8 x 16-32 K tokens)
+    // long contexts the tiles are ahead, 137 us against 154 for 8 x 16-32 K tokens)
     const bool few = max_query_len * group <= 16 && !(head_dim == 128 && block_size == 32 && span >= 4096);
     p.row_tiles = row_tiles;
     // Small calls, one wave of CTAs of at most eight key tiles each: clusters of
@@ -1273,6 +1274,12 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
         }
         return p;
     }
+    // Transposed from contexts on where an item's end weighs little (32 x 3-4 K
+    // tokens, 64 rows: 94 us against 119; 50 x 64 .. 2048 tokens of 40 kv heads,
+    // 27 rows at most: 171 against 166).
+    p.transposed = max_query_len * group <= 64 && head_dim == 128 && span >= 4096;
+    if (p.transposed)
+        tiles = (span + 127) / 128;
     p.shares = row_tiles > 1 ? 2 : 1;
     // two CTAs per SM, fewer where the largest such call has less to share out
     const int64_t units = items * row_tiles * (tiles + pkv::kTreeItemCost);
@@ -1289,10 +1296,10 @@ TreePlan tree_plan(int batch, int max_query_len, int num_heads, int num_kv_heads
     return p;
 }
 
-template <int D, int BS, bool BF16, bool CL>
+template <int D, int BS, bool BF16, bool CL, bool TR>
 cudaError_t configure_tree()
 {
-    auto kern = pkv::tree_attend_kernel<D, BS, BF16, CL>;
+    auto kern = pkv::tree_attend_kernel<D, BS, BF16, CL, TR>;
     static bool configured[64] = {};
     static std::mutex mu;
     const int dev = current_device();
@@ -1300,7 +1307,7 @@ cudaError_t configure_tree()
     if (dev >= 0 && dev < 64 && configured[dev])
         return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         pkv::TreeShape<D>::kSmemBytes);
+                                         pkv::TreeShape<D, TR>::kSmemBytes);
     if (e == cudaSuccess)   // two CTAs (and their TMEM) per SM
         e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  cudaSharedmemCarveoutMaxShared);
@@ -1309,34 +1316,36 @@ cudaError_t configure_tree()
     return e;
 }
 
-template <int D, int BS, bool BF16>
+template <int D, int BS, bool BF16, bool TR>
 cudaError_t launch_tree(const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a, const TreePlan &plan,
                         cudaStream_t st)
 {
-    constexpr int smem = pkv::TreeShape<D>::kSmemBytes;
-    if (plan.cluster) {
-        cudaError_t e = configure_tree<D, BS, BF16, true>();
-        if (e != cudaSuccess)
-            return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)plan.cluster, (unsigned)(a.batch * a.num_kv_heads * a.row_tiles));
-        cfg.blockDim = dim3(pkv::kTreeThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = (unsigned)plan.cluster;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, pkv::tree_attend_kernel<D, BS, BF16, true>, mq, cm.k, cm.v, cm.k4, cm.v4, a);
+    constexpr int smem = pkv::TreeShape<D, TR>::kSmemBytes;
+    if constexpr (!TR) {
+        if (plan.cluster) {
+            cudaError_t e = configure_tree<D, BS, BF16, true, false>();
+            if (e != cudaSuccess)
+                return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)plan.cluster, (unsigned)(a.batch * a.num_kv_heads * a.row_tiles));
+            cfg.blockDim = dim3(pkv::kTreeThreads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = st;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = (unsigned)plan.cluster;
+            attr[1].val.clusterDim.y = 1;
+            attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            return cudaLaunchKernelEx(&cfg, pkv::tree_attend_kernel<D, BS, BF16, true, false>, mq, cm.k, cm.v, cm.k4, cm.v4, a);
+        }
     }
-    cudaError_t e = configure_tree<D, BS, BF16, false>();
+    cudaError_t e = configure_tree<D, BS, BF16, false, TR>();
     if (e == cudaSuccess)
-        e = launch_pdl(pkv::tree_attend_kernel<D, BS, BF16, false>, dim3((unsigned)plan.ctas), dim3(pkv::kTreeThreads),
+        e = launch_pdl(pkv::tree_attend_kernel<D, BS, BF16, false, TR>, dim3((unsigned)plan.ctas), dim3(pkv::kTreeThreads),
                        smem, st, mq, cm.k, cm.v, cm.k4, cm.v4, a);
     if (e != cudaSuccess)
         return e;
@@ -1349,10 +1358,13 @@ template <bool BF16>
 cudaError_t dispatch_tree(int D, int bs, const CUtensorMap &mq, const CacheMaps &cm, const pkv::TreeArgs &a,
                           const TreePlan &plan, cudaStream_t st)
 {
-    if (D == 64 && bs == 16) return launch_tree<64, 16, BF16>(mq, cm, a, plan, st);
-    if (D == 64 && bs == 32) return launch_tree<64, 32, BF16>(mq, cm, a, plan, st);
-    if (D == 128 && bs == 16) return launch_tree<128, 16, BF16>(mq, cm, a, plan, st);
-    return launch_tree<128, 32, BF16>(mq, cm, a, plan, st);
+    if (D == 64 && bs == 16) return launch_tree<64, 16, BF16, false>(mq, cm, a, plan, st);
+    if (D == 64 && bs == 32) return launch_tree<64, 32, BF16, false>(mq, cm, a, plan, st);
+    if (plan.transposed)
+        return bs == 16 ? launch_tree<128, 16, BF16, true>(mq, cm, a, plan, st)
+                        : launch_tree<128, 32, BF16, true>(mq, cm, a, plan, st);
+    return bs == 16 ? launch_tree<128, 16, BF16, false>(mq, cm, a, plan, st)
+                    : launch_tree<128, 32, BF16, false>(mq, cm, a, plan, st);
 }
 
 }  // namespace
@@ -1484,10 +1496,12 @@ extern "C" pkv_status pkv_paged_attention_tree(
         return PKV_OK;
     }
     const bool two_q = max_query_len * group <= 64;
+    // (transposed: no more tokens than a tree has, the rows behind them stay zero)
+    const int q_box = two_q ? (plan.transposed ? max_query_len : 64 / group) : pkv::kTreeRows / group;
     CUtensorMap mq;
     CacheMaps cm;
     if ((s = make_query_map(&mq, query, num_tokens, num_heads, head_dim, group,
-                            (two_q ? 64 : pkv::kTreeRows) / group, dtype)) != PKV_OK ||
+                            q_box, dtype)) != PKV_OK ||
         (s = make_cache_maps(&cm, key_cache, value_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)) != PKV_OK)
         return s;
     pkv::TreeArgs a;
@@ -1511,6 +1525,7 @@ extern "C" pkv_status pkv_paged_attention_tree(
     a.num_blocks = (int)num_blocks;
     a.row_tiles = plan.row_tiles;
     a.shares = plan.shares;
+    a.q_box = q_box;
     a.q_slots = two_q ? 2 : 1;
     a.scale_log2 = scale_log2;
     const cudaError_t e = dtype == PKV_BF16 ? dispatch_tree<true>(head_dim, block_size, mq, cm, a, plan, st)

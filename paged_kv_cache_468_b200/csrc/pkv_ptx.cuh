@@ -78,6 +78,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// The same, bounded by a number of tries: one that fails takes 4 us, so 2^19 of
+// them about 2 s.  Half the instructions of the timed form, for kernels whose
+// warps wait at many places and run out of instruction cache (tree attention,
+// 256 sequences of 512 .. 640 tokens with 16 drafted each: 138 to 129 us).
+__device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity)
+{
+#pragma unroll 1
+    for (int i = 0; i < 1 << 19; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+    return false;
+}
+
 // ---- TMA (tensor, tiled, no multicast) ------------------------------------
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
@@ -299,6 +312,20 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64])
         : "memory");
 }
 
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr)
+{
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v)
+                 : "r"(taddr)
+                 : "memory");
+    return __uint_as_float(v);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
 {
     asm volatile(
@@ -329,6 +356,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+        "};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
 {
     asm volatile(

@@ -197,7 +197,11 @@ tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict_
 // with P over S in tensor memory, S double-buffered, and the running maximum m
 // moved only when a tile exceeds it by 2^8.  Only the last key tiles of a
 // sequence hold drafted keys: they alone are masked, by 64 bits per row cut
-// from the row's mask words.
+// from the row's mask words.  A tile's scores are read twice, for the maximum
+// and, 32 at a time by a loop, for the weights: less code and no spills, since
+// the warps' different work fills the instruction cache (256 sequences of 512
+// .. 640 tokens, 32/8 heads, 8 and 32 nodes: 120 and 166 us with the weights of
+// 64 keys unrolled, 117 and 160 so; 8 of 16-32 K tokens and 64 nodes 283, 285).
 //
 // Work.  The keys are read once per (sequence, kv head) if one row tile covers
 // its rows, so the floor of such calls is the cache's bytes over the memory
@@ -222,9 +226,30 @@ tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict_
 // memory: one kernel, no workspace.
 //
 // A masked tile is the only one whose V rows some row may not see: such a row
-// gives them weight 0, and 0 times an infinity or a NaN would poison it.  The
-// softmax warps look through the V rows of masked tiles; where one holds such
-// a value, they zero it in shared memory and add it to the rows that do see it.
+// gives them weight 0, and 0 times an infinity or a NaN would poison it.  Warp 7
+// looks through the V rows of masked tiles; where one holds such a value, it
+// zeroes it in shared memory and the softmax warps add it to the rows that do
+// see it.
+//
+// Up to 64 rows over long contexts (TR, head_dim 128) half of a 128-row tile's
+// products and weights and more would be for rows that do not exist, and
+// in a power-limited run they cost clock.  There the products are transposed:
+//
+//   S^T[keys x rows] = K_j Q^T,   O^T[D x rows] += V_j^T P_j^T
+//
+// 128 keys to a tile and 64 rows as the products' N.  A softmax thread is a
+// key, so a row's maximum is the CTA's: it lies in shared memory, all weights
+// of a tile are taken against it, and the four warps vote whether a score lies
+// more than 2^14 above it; only then (seldom: a part starts with its first
+// key's scores) the true maxima are worked out by exchanges.  Row sums stay
+// spread over the threads, by mma.sync products of the weights' registers with
+// ones.  P^T goes through shared memory as the second product's B; V^T is its
+// A, with head_dim along the rows as it lies.  A part's end is dearer than
+// with 128-row tiles (2-byte stores, a column of the head per thread), the
+// tile half as dear: 32 sequences of 3-4 K tokens, 32/8 heads, 8 nodes 88 us
+// against 94, 16 nodes 94 against 119 (sustained 99, 113); 8 of 16-32 K and 16
+// nodes 140 against 149 (sustained 154, 178); at 512 .. 640 tokens and 10 nodes
+// 170 against 127, level near 1000 tokens.
 struct TreeArgs {
     const int32_t *query_start;      // [batch + 1]
     const int32_t *tree_mask;        // [T, words]
@@ -246,6 +271,7 @@ struct TreeArgs {
     int num_blocks;
     int row_tiles;                   // of the largest tree (CL: items are (sequence, kv head, row tile))
     int shares;                      // 2: pairs of row tiles, then single ones; 1: single ones only
+    int q_box;                       // query tokens that a Q copy brings
     int q_slots;                     // 2: two Q buffers of 64 rows (no item has more), 1: one of 128
     float scale_log2;
 };
@@ -259,25 +285,32 @@ constexpr int kTreeMinUnits = 2;         // a CTA's share is not cut below this
 constexpr int kTreeParts = 6;            // queue of parts between a CTA's warps
 constexpr int kTreeScans = 8;            // masked tiles whose scan result is kept
 
-template <int D>
+// Shared memory and barriers of a CTA; TR: of the transposed products.
+template <int D, bool TR>
 struct TreeShape {
     static constexpr int kHalves = D / 64;
-    static constexpr int kQHalf = kTreeRows * 128;
-    static constexpr int kKVHalf = kTreeKeys * 128;
-    static constexpr int kQBytes = kHalves * kQHalf;
-    static constexpr int kKVBytes = kHalves * kKVHalf;
+    static constexpr int kKeys = TR ? 128 : kTreeKeys;           // keys per tile; V comes 64 at a time
+    // two Q buffers of 64 rows: one after the other TR, else the halves of each 64-column half
+    static constexpr int kQHalf = (TR ? 64 : kTreeRows) * 128;
+    static constexpr int kQSlot = TR ? kHalves * kQHalf : 64 * 128;
+    static constexpr int kQBytes = kHalves * kTreeRows * 128;
+    static constexpr int kKHalf = kKeys * 128;
+    static constexpr int kKBytes = kHalves * kKHalf;
+    static constexpr int kVHalf = kTreeKeys * 128;
+    static constexpr int kVBytes = kHalves * kVHalf;
     // two CTAs per SM: 112 KB each for D = 128 (32 + 80), 96 KB for D = 64 (16 + 80)
-    static constexpr int kKStages = D == 128 ? 3 : 6;
+    static constexpr int kKStages = TR ? 1 : (D == 128 ? 3 : 6);
     static constexpr int kVStages = D == 128 ? 2 : 4;
     static constexpr int kKOff = kQBytes;
-    static constexpr int kVOff = kKOff + kKStages * kKVBytes;
-    static constexpr int kDataBytes = kVOff + kVStages * kKVBytes;
+    static constexpr int kVOff = kKOff + kKStages * kKBytes;
+    static constexpr int kPOff = kVOff + kVStages * kVBytes;     // TR: the weights, 128 keys x 64 rows
+    static constexpr int kDataBytes = kPOff + (TR ? 128 * 128 : 0);
     static constexpr int kSmemBytes = kDataBytes + 1024;
     // barriers
     static constexpr int kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = kKFull + kKStages, kVFull = kKEmpty + kKStages,
                          kVEmpty = kVFull + kVStages, kScanReq = kVEmpty + kVStages, kScanned = kScanReq + 1, kSFull = kScanned + 1,
-                         kPFull = kSFull + 2, kODone = kPFull + 2, kDrain = kODone + 1, kPartFull = kDrain + 1,
-                         kPartEmpty = kPartFull + kTreeParts, kNumBars = kPartEmpty + kTreeParts;
+                         kPFull = kSFull + 2, kODone = kPFull + 2, kDrain = kODone + 1, kVote = kDrain + 1, kShare = kVote + 1,
+                         kPartFull = kShare + 1, kPartEmpty = kPartFull + kTreeParts, kNumBars = kPartEmpty + kTreeParts;
 };
 
 // A part of an item: key tiles k0 .. k1 - 1 of `tiles` for one row tile of a
@@ -302,28 +335,28 @@ __device__ __forceinline__ int tree_items(int n, int G, int shares, int share)
 }
 // Units of sequence b (0 where it contradicts itself).  The host keeps the
 // total below 2^31.
-template <int BS>
+template <int BS, int KEYS>
 __device__ __forceinline__ int tree_units(const TreeArgs &a, int b, int share, TreeSeq *s)
 {
     if (!tree_seq(a.query_start, a.context_lens, b, a.num_tokens, a.max_query_len, a.max_blocks * BS, s))
         return -1;
     return tree_items(s->n, a.group, a.shares, share) * a.num_kv_heads *
-           ((s->len + kTreeKeys - 1) / kTreeKeys + kTreeItemCost);
+           ((s->len + KEYS - 1) / KEYS + kTreeItemCost);
 }
 
-template <int BS>
+template <int BS, int KEYS>
 __device__ __forceinline__ bool tree_next(TreeWalk &w, const TreeArgs &a, int share, int member, TreePart *p)
 {
     while (w.g < w.end) {
         TreeSeq q;
-        const int units = max(0, tree_units<BS>(a, w.b, share, &q));
+        const int units = max(0, tree_units<BS, KEYS>(a, w.b, share, &q));
         const int off = w.g - w.seq0;
         if (off >= units) {
             w.seq0 += units;
             ++w.b;
             continue;
         }
-        const int tiles = (q.len + kTreeKeys - 1) / kTreeKeys;
+        const int tiles = (q.len + KEYS - 1) / KEYS;
         const int cost = tiles + kTreeItemCost;
         const int item = off / cost;
         const int k0 = off - item * cost;
@@ -406,6 +439,38 @@ __device__ __forceinline__ uint32_t fma_zero2(uint32_t x, uint32_t acc)
     return acc;
 }
 
+// (a NaN stays)
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// TR: the query rows (bit c: row c) that see the key in cell `cell` of the
+// block whose first position is p0 (no row: a cell that holds none).
+template <int BS, int UNROLL>
+__device__ __forceinline__ uint64_t tree_rows_that_see(const int32_t *mask, int words, int G, int n, int len, int p0, int cell)
+{
+    const int tail = len % BS;
+    if (p0 >= len)
+        return 0ull;
+    if (tail && p0 + BS > len)
+        cell -= BS - tail;                   // a partly filled last block ends its slot
+    if (cell < 0)
+        return 0ull;
+    const int j = p0 + cell - (len - n);
+    if (j < 0)
+        return ~0ull;
+    mask += j >> 5;
+    const uint64_t rows = (1ull << G) - 1ull;            // (G <= 8)
+    uint64_t v = 0ull;
+#pragma unroll UNROLL
+    for (int i = 0; i < n; ++i)
+        v |= ((uint32_t)__ldg(mask + (size_t)i * words) >> (j & 31)) & 1u ? rows << (i * G) : 0ull;
+    return v;
+}
+
 // O_row += the infinities and NaN of V's rows of key tile t that the row sees
 // (they were zeroed in shared memory).  Rare, so simple: one key at a time,
 // read from the cache again.
@@ -447,9 +512,37 @@ __device__ __noinline__ void tree_add_nonfinite(const uint16_t *value_cache, con
     tmem_wait_st();
 }
 
-// Warps: 0-3 softmax and output (warp w owns TMEM lanes 32 w ..), 4 K loads,
-// 5 MMA issue, 6 V loads, 7 the parts' queue, Q loads and the scan of masked
-// tiles' V rows.
+// The same for the transposed products: thread = column `col` of the head, the
+// tile's 128 keys one at a time, query row c in TMEM column c.  (Inline and
+// few registers: a call here had the key loop's registers spilled.)
+template <int BS, bool BF16>
+__device__ __forceinline__ void tree_add_nonfinite_t(const uint16_t *value_cache, const int32_t *table, int num_blocks, int kvs, int kvh,
+                                                     const int32_t *mask, int words, int G, int n, int len, int t, int col, uint32_t tO)
+{
+#pragma unroll 1
+    for (int k = 0; k < 128; ++k) {
+        const int p0 = t * 128 + k / BS * BS;
+        uint64_t vis = tree_rows_that_see<BS, 1>(mask, words, G, n, len, p0, k % BS) & (~0ull >> (64 - n * G));
+        if (vis == 0ull)
+            continue;
+        const int tail = len % BS;
+        const int cell = k % BS - (tail && p0 + BS > len ? BS - tail : 0);
+        int blk = __ldg(table + p0 / BS);
+        blk = (unsigned)blk < (unsigned)num_blocks ? blk : 0;
+        const uint32_t x = __ldg(value_cache + (((size_t)blk * BS + cell) * kvs + kvh) * 128 + col);
+        const bool bad = nonfinite2<BF16>(x) & 1u;
+        if (!__any_sync(0xffffffffu, bad))
+            continue;
+        const float y = bad ? unpack2<BF16>(x).x : 0.f;
+        for (; vis; vis &= vis - 1ull) {
+            const uint32_t at = tO + (uint32_t)__ffsll((long long)vis) - 1u;
+            const float o = tmem_ld1(at);
+            tmem_st1(at, bad ? o + y : o);
+            tmem_wait_st();
+        }
+    }
+}
+
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -478,14 +571,19 @@ __device__ __forceinline__ float2 cluster_load2(uint32_t addr)
     return v;
 }
 
-template <int D, int BS, bool BF16, bool CL>
+// Warps: 0-3 softmax and output (warp w owns TMEM lanes 32 w ..), 4 K loads,
+// 5 MMA issue, 6 V loads, 7 the parts' queue, Q loads and the scan of masked
+// tiles' V rows.
+template <int D, int BS, bool BF16, bool CL, bool TR>
 __global__ void __launch_bounds__(kTreeThreads, 2)
 tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k4,
                    const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ TreeArgs a)
 {
-    using Sh = TreeShape<D>;
-    constexpr int KS = D / 16, KV_STEPS = kTreeKeys / 16, BPT = kTreeKeys / BS;
+    using Sh = TreeShape<D, TR>;
+    static_assert(!TR || (D == 128 && !CL), "the transposed products have head_dim as M; clusters have few tiles");
+    constexpr int KEYS = Sh::kKeys;
+    constexpr int KS = D / 16, KV_STEPS = kTreeKeys / 16;
     constexpr uint32_t kTmemCols = 256;          // S/P: 2 x 64 columns, O: D columns at 128
     // The dynamic shared memory is all that the kernel has, so it starts on the
     // 1024-byte boundary that the swizzled tiles need; what else the CTA keeps
@@ -496,6 +594,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int total[2];
         int scan[kTreeThreads / 32];
         uint32_t bad[kTreeScans];
+        uint32_t vote[2][4];
+        alignas(16) float m[TR ? 64 : 4];
         uint32_t tmem;
         TreePart part[kTreeParts];
     };
@@ -518,7 +618,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (threadIdx.x < Sh::kNumBars) {
         const int i = threadIdx.x;
         // P: one arrival per softmax warp; a part is read by K, V and MMA warps and the softmax warps
-        const int count = i >= Sh::kPFull && i < Sh::kPFull + 2 ? 4 : (i >= Sh::kPartEmpty ? 7 : 1);
+        const int count = (i >= Sh::kPFull && i < Sh::kPFull + 2) || i == Sh::kVote || i == Sh::kShare
+                              ? 4 : (i >= Sh::kPartEmpty ? 7 : 1);
         mbar_init(bar(i), count);
     }
     if (threadIdx.x == 128) {
@@ -529,11 +630,17 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         prefetch_tensormap(&tm_v4);
     }
     fence_mbar_init();
-    // masked columns of a tile may meet V rows that no load has filled
+    // masked columns of a tile may meet V rows that no load has filled; TR: so
+    // may Q rows and weights past the tree's rows, and zeros cost least power
     {
         uint4 *vr = reinterpret_cast<uint4 *>(data + Sh::kVOff);
-        for (int i = threadIdx.x; i < Sh::kVStages * Sh::kKVBytes / 16; i += kTreeThreads)
+        for (int i = threadIdx.x; i < (Sh::kDataBytes - Sh::kVOff) / 16; i += kTreeThreads)
             vr[i] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (TR) {
+            uint4 *qr = reinterpret_cast<uint4 *>(data);
+            for (int i = threadIdx.x; i < Sh::kQBytes / 16; i += kTreeThreads)
+                qr[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
         fence_proxy_async_smem();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -555,7 +662,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!good && threadIdx.x == 0 && blockIdx.x == 0 && rt == 0 && kvh == 0)
             raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
         const int rows = good ? min(R, q.n * G - rt * R) : 0;
-        const int tiles = rows > 0 ? (q.len + kTreeKeys - 1) / kTreeKeys : 0;
+        const int tiles = rows > 0 ? (q.len + KEYS - 1) / KEYS : 0;
         if (threadIdx.x == 0) {
             TreePart p{b, kvh, rt, 0, q.q0, q.n, q.len, tiles, tiles * (int)blockIdx.x / P, tiles * ((int)blockIdx.x + 1) / P};
             if (p.k0 == p.k1)
@@ -584,7 +691,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int mine = 0;
         for (int b = b0; b < b1; ++b) {
             TreeSeq q;
-            const int u = tree_units<BS>(a, b, share, &q);
+            const int u = tree_units<BS, KEYS>(a, b, share, &q);
             if (u < 0 && blockIdx.x == 0 && share == 0)
                 raise_flag(PKV_DEVFLAG_CONTEXT_RANGE);
             mine += max(u, 0);
@@ -616,7 +723,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int at = upto - mine, b = b0;
             for (;; ++b) {
                 TreeSeq q;
-                const int u = max(0, tree_units<BS>(a, b, share, &q));
+                const int u = max(0, tree_units<BS, KEYS>(a, b, share, &q));
                 if (g0 < at + u)
                     break;
                 at += u;
@@ -640,7 +747,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     int part_i = 0;
     auto next_part = [&](TreePart *p, bool one) -> bool {
         const int slot = part_i % kTreeParts;
-        bool got = mbar_wait_bounded(bar(Sh::kPartFull + slot), (uint32_t)((part_i / kTreeParts) & 1), kWaitLimitNs);
+        bool got = mbar_wait_tries(bar(Sh::kPartFull + slot), (uint32_t)((part_i / kTreeParts) & 1));
         if (!one)
             got = __all_sync(0xffffffffu, got);
         if (!got) {
@@ -677,15 +784,19 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int tail = s.len % BS;
             const int32_t *trow = a.block_tables + (size_t)s.b * a.max_blocks;
             int ids = 0, have = -1;                  // block ids of the 32-entry window `have`
-            for (int t = s.k0; t < s.k1; ++t, ++J) {
-                const int kb0 = t * BPT;             // a tile's ids lie in one window
-                const int nb = min(BPT, nblk - kb0);
+            // K by tiles, V by 64 keys
+            const int bpt = (is_k ? KEYS : kTreeKeys) / BS;
+            const int per = is_k ? 1 : KEYS / kTreeKeys;
+            const int t1 = is_k ? s.k1 : min(s.k1 * per, (s.len + kTreeKeys - 1) / kTreeKeys);
+            for (int t = s.k0 * per; t < t1; ++t, ++J) {
+                const int kb0 = t * bpt;             // a tile's ids lie in one window
+                const int nb = min(bpt, nblk - kb0);
                 if ((kb0 & ~31) != have) {
                     have = kb0 & ~31;
                     ids = have + lane < nblk ? __ldg(trow + have + lane) : 0;
                 }
                 if (J >= NS) {
-                    const bool free_ = mbar_wait_bounded(bar(empty0 + st), (uint32_t)((round - 1) & 1), kWaitLimitNs);
+                    const bool free_ = mbar_wait_tries(bar(empty0 + st), (uint32_t)((round - 1) & 1));
                     if (!__all_sync(0xffffffffu, free_)) {
                         ok = false;
                         break;
@@ -695,7 +806,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mbar_arrive_expect_tx(bar(full0 + st), (uint32_t)(nb * BS * D * 2));
                 __syncwarp();
                 const int i = lane / Sh::kHalves, h = lane % Sh::kHalves;
-                int blk = __shfl_sync(0xffffffffu, ids, (kb0 + min(i, BPT - 1)) & 31);
+                int blk = __shfl_sync(0xffffffffu, ids, (kb0 + min(i, bpt - 1)) & 31);
                 if (i < nb) {
                     if ((unsigned)blk >= (unsigned)a.num_blocks) {
                         if (h == 0)
@@ -704,7 +815,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     // a partly filled last block ends at its slot's last row; the rows before read as zero
                     const int shift = tail && kb0 + i == nblk - 1 ? tail - BS : 0;
-                    const uint32_t dst = ring + st * Sh::kKVBytes + h * Sh::kKVHalf + i * BS * 128;
+                    const uint32_t dst = ring + st * (is_k ? Sh::kKBytes : Sh::kVBytes) + h * (is_k ? Sh::kKHalf : Sh::kVHalf) + i * BS * 128;
                     if (shift)
                         tma_load_4d(dst, tm4, bar(full0 + st), h * 64, s.kvh, shift, blk, policy);
                     else
@@ -721,7 +832,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // copies still in flight land before the CTA can exit
         if (lane == 0)
             for (int j = J > NS ? J - NS : 0; j < J; ++j)
-                mbar_wait_bounded(bar(full0 + j % NS), (uint32_t)((j / NS) & 1), kWaitLimitNs / 8);
+                mbar_wait_tries(bar(full0 + j % NS), (uint32_t)((j / NS) & 1));
         if (!CL && is_k && lane < a.shares) {
             // An item that started in the share before and goes on in this one:
             // the merge finds its records through this share.
@@ -733,13 +844,13 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int4 d = make_int4(0, 0, 0, 0);
             TreeWalk w = loc->walk[share];
             TreeSeq q;
-            if (c > 0 && w.g < w.end && tree_units<BS>(a, w.b, share, &q) > 0) {
-                const int tiles = (q.len + kTreeKeys - 1) / kTreeKeys;
+            if (c > 0 && w.g < w.end && tree_units<BS, KEYS>(a, w.b, share, &q) > 0) {
+                const int tiles = (q.len + KEYS - 1) / KEYS;
                 const int k0 = (w.g - w.seq0) % (tiles + kTreeItemCost);
                 const int start = w.g - k0;          // the item's first unit
                 TreePart p;
                 if (k0 > 0 && k0 < tiles && start >= tree_cut(total, c - 1, n) &&
-                    tree_next<BS>(w, a, share, blockIdx.x & 1, &p)) {
+                    tree_next<BS, KEYS>(w, a, share, blockIdx.x & 1, &p)) {
                     // the last CTA (or pair) with keys of the item: about (its end) n / total
                     int last = (int)min((int64_t)(n - 1), (int64_t)(start + tiles) * n / total);
                     while (tree_cut(total, last, n) >= start + tiles)
@@ -763,13 +874,13 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         auto make = [&]() {                          // queue part `made`
             const int slot = made % kTreeParts;
             if (made >= kTreeParts &&
-                !__all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kPartEmpty + slot),
-                                                           (uint32_t)((made / kTreeParts - 1) & 1), kWaitLimitNs))) {
+                !__all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kPartEmpty + slot),
+                                                           (uint32_t)((made / kTreeParts - 1) & 1)))) {
                 ok = false;
                 return;
             }
             TreePart p;
-            while (!tree_next<BS>(walk, a, share, blockIdx.x & 1, &p)) {
+            while (!tree_next<BS, KEYS>(walk, a, share, blockIdx.x & 1, &p)) {
                 if (++share >= a.shares) {
                     done = true;
                     p.k1 = 0;
@@ -787,17 +898,15 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         auto load_q = [&](int u, const TreePart &p) {
             const int slot = two_q ? u & 1 : 0;
             const int turn = two_q ? u >> 1 : u;
-            if (turn > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kQEmpty + slot), (uint32_t)((turn - 1) & 1),
-                                                                       kWaitLimitNs))) {
+            if (turn > 0 && !__all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kQEmpty + slot), (uint32_t)((turn - 1) & 1)))) {
                 ok = false;
                 return;
             }
             if (lane == 0) {
-                const int rows = (two_q ? 64 / G : TT) * G;
-                mbar_arrive_expect_tx(bar(Sh::kQFull + slot), (uint32_t)(Sh::kHalves * rows * 128));
+                mbar_arrive_expect_tx(bar(Sh::kQFull + slot), (uint32_t)(Sh::kHalves * a.q_box * G * 128));
 #pragma unroll
                 for (int h = 0; h < Sh::kHalves; ++h)
-                    tma_load_3d(sQ + h * Sh::kQHalf + slot * 64 * 128, &tm_q, bar(Sh::kQFull + slot), h * 64, p.kvh * G,
+                    tma_load_3d(sQ + h * Sh::kQHalf + slot * Sh::kQSlot, &tm_q, bar(Sh::kQFull + slot), h * 64, p.kvh * G,
                                 p.q0 + p.rt * TT, policy);
             }
             __syncwarp();
@@ -823,48 +932,54 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             for (int t = s.k0; ok && t < s.k1; ++t) {
-                if ((t + 1) * kTreeKeys > s.len - s.n) {
-                    // the MMA thread asks for it when the tile's V has landed: this
-                    // warp's place in the tiles says nothing of the V ring's
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kScanReq), (uint32_t)(scans & 1), kWaitLimitNs) &&
-                                                        mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs))) {
-                        ok = false;
-                        break;
-                    }
-                    // V rows that some query row may not see: from the first drafted
-                    // key on (a shifted last block puts it further on), four at a time
-                    const int i0 = max(0, s.len - s.n - t * kTreeKeys) / 4;
-                    uint4 *vt = reinterpret_cast<uint4 *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
-                    uint32_t any[4] = {0u, 0u, 0u, 0u};
+                const bool masked = (t + 1) * KEYS > s.len - s.n;
+                // the MMA thread asks for it when the tile's V has landed: this
+                // warp's place in the tiles says nothing of the V ring's
+                if (masked && !__all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kScanReq), (uint32_t)(scans & 1)))) {
+                    ok = false;
+                    break;
+                }
+                bool bad = false;
+                for (int v = t * (KEYS / kTreeKeys); v < (t + 1) * (KEYS / kTreeKeys) && v * kTreeKeys < s.len; ++v) {
+                    if (masked) {
+                        mbar_wait_tries(bar(Sh::kVFull + vs), (uint32_t)(vround & 1));   // (has landed)
+                        // V rows that some query row may not see: from the first drafted
+                        // key on (a shifted last block puts it further on), four at a time
+                        const int i0 = max(0, s.len - s.n - v * kTreeKeys) / 4;
+                        uint4 *vt = reinterpret_cast<uint4 *>(data + Sh::kVOff + vs * Sh::kVBytes) + lane;
+                        uint32_t any[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 4
-                    for (int i = i0 * Sh::kHalves; i < Sh::kKVBytes / 512; ++i) {
-                        // (the rows of the 64-column halves in turn)
-                        const int row4 = i / Sh::kHalves, h = i - row4 * Sh::kHalves;
-                        const uint4 x = vt[h * (Sh::kKVHalf / 16) + row4 * 32];
-                        any[0] = fma_zero2<BF16>(x.x, any[0]);
-                        any[1] = fma_zero2<BF16>(x.y, any[1]);
-                        any[2] = fma_zero2<BF16>(x.z, any[2]);
-                        any[3] = fma_zero2<BF16>(x.w, any[3]);
-                    }
-                    // (a sum of zeros is 0 or -0)
-                    const bool bad = __any_sync(0xffffffffu, ((any[0] | any[1] | any[2] | any[3]) & 0x7fff7fffu) != 0u);
-                    if (bad) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(data + Sh::kVOff + vs * Sh::kKVBytes) + lane;
+                        for (int i = i0 * Sh::kHalves; i < Sh::kVBytes / 512; ++i) {
+                            // (the rows of the 64-column halves in turn)
+                            const int row4 = i / Sh::kHalves, h = i - row4 * Sh::kHalves;
+                            const uint4 x = vt[h * (Sh::kVHalf / 16) + row4 * 32];
+                            any[0] = fma_zero2<BF16>(x.x, any[0]);
+                            any[1] = fma_zero2<BF16>(x.y, any[1]);
+                            any[2] = fma_zero2<BF16>(x.z, any[2]);
+                            any[3] = fma_zero2<BF16>(x.w, any[3]);
+                        }
+                        // (a sum of zeros is 0 or -0)
+                        if (__any_sync(0xffffffffu, ((any[0] | any[1] | any[2] | any[3]) & 0x7fff7fffu) != 0u)) {
+                            bad = true;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(data + Sh::kVOff + vs * Sh::kVBytes) + lane;
 #pragma unroll 1
-                        for (int i = 0; i < Sh::kKVBytes / 128; ++i)
-                            w[i * 32] &= ~(nonfinite2<BF16>(w[i * 32]) * 0xffffu);
-                        fence_proxy_async_smem();
+                            for (int i = 0; i < Sh::kVBytes / 128; ++i)
+                                w[i * 32] &= ~(nonfinite2<BF16>(w[i * 32]) * 0xffffu);
+                            fence_proxy_async_smem();
+                        }
                     }
+                    if (++vs == Sh::kVStages) {
+                        vs = 0;
+                        ++vround;
+                    }
+                }
+                if (masked) {
                     __syncwarp();
                     if (lane == 0) {
                         loc->bad[scans % kTreeScans] = bad;
                         mbar_arrive(bar(Sh::kScanned));
                     }
                     ++scans;
-                }
-                if (++vs == Sh::kVStages) {
-                    vs = 0;
-                    ++vround;
                 }
             }
             ++u;
@@ -874,8 +989,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // the last Q loads land before the CTA can exit
         if (lane == 0)
             for (int i = max(0, loaded - (two_q ? 2 : 1)); i < loaded; ++i)
-                mbar_wait_bounded(bar(Sh::kQFull + (two_q ? i & 1 : 0)), (uint32_t)((two_q ? i >> 1 : i) & 1), kWaitLimitNs / 8);
-    } else if (warp == 5) {
+                mbar_wait_tries(bar(Sh::kQFull + (two_q ? i & 1 : 0)), (uint32_t)((two_q ? i >> 1 : i) & 1));
+    } else if (!TR && warp == 5) {
         // ---- MMA issue: one thread ----
         if (lane == 0) {
             constexpr uint32_t idS = f16_idesc<BF16>(kTreeRows, kTreeKeys, false);
@@ -883,11 +998,11 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             int ks_ = 0, kround = 0;                 // K stage of the next S
             // S of global tile J; u: its part (Q buffer); last: the part's last S
             auto k_ready = [&]() -> bool {
-                return mbar_wait_bounded(bar(Sh::kKFull + ks_), (uint32_t)(kround & 1), kWaitLimitNs);
+                return mbar_wait_tries(bar(Sh::kKFull + ks_), (uint32_t)(kround & 1));
             };
             auto issue_s = [&](int J, int u, bool last) {
                 tc_fence_after();
-                const uint32_t kt = sK + ks_ * Sh::kKVBytes;
+                const uint32_t kt = sK + ks_ * Sh::kKBytes;
                 // with two Q buffers the rows past a buffer's 64 read what lies
                 // behind it: rows that nobody reads
                 const uint32_t qt = sQ + (two_q ? (u & 1) * 64 * 128 : 0);
@@ -895,7 +1010,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint32_t koff = (uint32_t)((ks & 3) * 32);
                     tc_mma_f16(tmem + (J & 1) * kTreeKeys, sw128_desc(qt + (ks >> 2) * Sh::kQHalf + koff, 16, 1024),
-                               sw128_desc(kt + (ks >> 2) * Sh::kKVHalf + koff, 16, 1024), idS, ks > 0 ? 1u : 0u);
+                               sw128_desc(kt + (ks >> 2) * Sh::kKHalf + koff, 16, 1024), idS, ks > 0 ? 1u : 0u);
                 }
                 tc_commit(bar(Sh::kSFull + (J & 1)));
                 tc_commit(bar(Sh::kKEmpty + ks_));
@@ -907,8 +1022,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             };
             auto q_ready = [&](int u) -> bool {
-                return mbar_wait_bounded(bar(Sh::kQFull + (two_q ? u & 1 : 0)), (uint32_t)((two_q ? u >> 1 : u) & 1),
-                                         kWaitLimitNs);
+                return mbar_wait_tries(bar(Sh::kQFull + (two_q ? u & 1 : 0)), (uint32_t)((two_q ? u >> 1 : u) & 1));
             };
             TreePart s, nx;
             bool has = next_part(&s, true), has_nx = has && next_part(&nx, true);
@@ -929,29 +1043,29 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const bool ahead = !last || (has_nx && two_q);
                     // what has landed long since is looked at first: each look
                     // costs 100-200 cycles, and P_{J-1} V_{J-1} runs meanwhile
-                    ok = mbar_wait_bounded(bar(Sh::kVFull + vs), (uint32_t)(vround & 1), kWaitLimitNs);
+                    ok = mbar_wait_tries(bar(Sh::kVFull + vs), (uint32_t)(vround & 1));
                     const bool scan = j >= first_masked;
                     if (ok && scan)
                         mbar_arrive(bar(Sh::kScanReq));      // warp 7 scans V while the softmax works
                     if (ok && ahead) {
                         ok = (!last || q_ready(u + 1)) && k_ready() &&
-                             (J == 0 || mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs));
+                             (J == 0 || mbar_wait_tries(bar(Sh::kODone), (uint32_t)((J - 1) & 1)));
                         if (ok)
                             issue_s(J + 1, last ? u + 1 : u, last ? nx.k1 - nx.k0 == 1 : j + 2 == cnt);
                     }
                     if (ok && scan) {
-                        ok = mbar_wait_bounded(bar(Sh::kScanned), (uint32_t)(scans & 1), kWaitLimitNs);
+                        ok = mbar_wait_tries(bar(Sh::kScanned), (uint32_t)(scans & 1));
                         ++scans;
                     }
-                    ok = ok && mbar_wait_bounded(bar(Sh::kPFull + (J & 1)), (uint32_t)((J >> 1) & 1), kWaitLimitNs);
+                    ok = ok && mbar_wait_tries(bar(Sh::kPFull + (J & 1)), (uint32_t)((J >> 1) & 1));
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t vt = sV + vs * Sh::kKVBytes;
+                    const uint32_t vt = sV + vs * Sh::kVBytes;
                     const uint32_t tp = tmem + (J & 1) * kTreeKeys;
 #pragma unroll
                     for (int kk = 0; kk < KV_STEPS; ++kk)
-                        tc_mma_f16_ts(tO, tp + kk * 8, sw128_desc(vt + kk * 16 * 128, Sh::kKVHalf, 1024), idO,
+                        tc_mma_f16_ts(tO, tp + kk * 8, sw128_desc(vt + kk * 16 * 128, Sh::kVHalf, 1024), idO,
                                       (j > 0 || kk > 0) ? 1u : 0u);
                     tc_commit(bar(Sh::kODone));
                     tc_commit(bar(Sh::kVEmpty + vs));
@@ -963,7 +1077,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         // O_DONE of this tile: it completes after the MMAs that read
                         // the buffer, and a wait for the phase before could miss it
                         if (!(ok = q_ready(u + 1) && k_ready() &&
-                                   mbar_wait_bounded(bar(Sh::kODone), (uint32_t)(J & 1), kWaitLimitNs)))
+                                   mbar_wait_tries(bar(Sh::kODone), (uint32_t)(J & 1))))
                             break;
                         issue_s(J + 1, u + 1, nx.k1 - nx.k0 == 1);
                     }
@@ -978,8 +1092,422 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok)
                 raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
             tc_commit(bar(Sh::kDrain));
-            mbar_wait_bounded(bar(Sh::kDrain), 0u, kWaitLimitNs);
+            mbar_wait_tries(bar(Sh::kDrain), 0u);
         }
+    } else if (warp == 5) {
+        // ---- TR: MMA issue, one thread ----
+        if (lane == 0) {
+            constexpr uint32_t idS = f16_idesc<BF16>(128, 64, false);
+            constexpr uint32_t idO = f16_idesc<BF16>(128, 64, true) | (1u << 15);   // A = V^T: M (head_dim) along its rows
+            TreePart s, nx;
+            bool has = next_part(&s, true), has_nx = has && next_part(&nx, true);
+            bool ok = true;
+            int J = 0, u = 0, vs = 0, vround = 0, scans = 0;
+            auto q_ready = [&](int u) -> bool {
+                return mbar_wait_tries(bar(Sh::kQFull + (u & 1)), (uint32_t)((u >> 1) & 1));
+            };
+            auto k_ready = [&](int J) -> bool { return mbar_wait_tries(bar(Sh::kKFull), (uint32_t)(J & 1)); };
+            // S^T of global tile J (part u; last: the part's last): buffer J & 1
+            auto issue_s = [&](int J, int u, bool last) {
+                tc_fence_after();
+                const uint32_t qt = sQ + (u & 1) * Sh::kQSlot;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t koff = (uint32_t)((ks & 3) * 32);
+                    tc_mma_f16(tmem + (J & 1) * 64, sw128_desc(sK + (ks >> 2) * Sh::kKHalf + koff, 16, 1024),
+                               sw128_desc(qt + (ks >> 2) * Sh::kQHalf + koff, 16, 1024), idS, ks > 0 ? 1u : 0u);
+                }
+                tc_commit(bar(Sh::kSFull + (J & 1)));
+                tc_commit(bar(Sh::kKEmpty));
+                if (last)
+                    tc_commit(bar(Sh::kQEmpty + (u & 1)));
+            };
+            if (has && (ok = q_ready(0) && k_ready(0)))
+                issue_s(0, 0, s.k1 - s.k0 == 1);
+            while (ok && has) {
+                const int first_masked = (s.len - s.n) / KEYS;
+                for (int t = s.k0; t < s.k1; ++t, ++J) {
+                    const bool last = t + 1 == s.k1;
+                    const int subs = min(2, (s.len - t * KEYS + kTreeKeys - 1) / kTreeKeys);   // 64-key halves with keys
+                    if (!last || has_nx) {
+                        // the next S^T: its buffer was read before P_{J-1} was handed over
+                        ok = (!last || q_ready(u + 1)) && k_ready(J + 1);
+                        if (!ok)
+                            break;
+                        issue_s(J + 1, last ? u + 1 : u, last ? nx.k1 - nx.k0 == 1 : t + 2 == s.k1);
+                    }
+                    for (int h = 0; ok && h < subs; ++h) {
+                        const int st = (vs + h) % Sh::kVStages, round = vround + (vs + h) / Sh::kVStages;
+                        ok = mbar_wait_tries(bar(Sh::kVFull + st), (uint32_t)(round & 1));
+                    }
+                    if (ok && t >= first_masked) {
+                        mbar_arrive(bar(Sh::kScanReq));      // warp 7 scans V while the softmax works
+                        ok = mbar_wait_tries(bar(Sh::kScanned), (uint32_t)(scans & 1));
+                        ++scans;
+                    }
+                    ok = ok && mbar_wait_tries(bar(Sh::kPFull), (uint32_t)(J & 1));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    // O^T += V^T P^T, 16 keys per step: V^T (head_dim along the rows
+                    // of V, halves kVHalf apart) and P^T (query rows along its rows)
+                    for (int h = 0; h < subs; ++h) {
+                        const uint32_t vt = sV + vs * Sh::kVBytes, pt = data_s + Sh::kPOff + h * 64 * 128;
+#pragma unroll
+                        for (int kk = 0; kk < KV_STEPS; ++kk)
+                            tc_mma_f16(tO, sw128_desc(vt + kk * 16 * 128, Sh::kVHalf, 1024),
+                                       sw128_desc(pt + kk * 16 * 128, 1024, 1024), idO, (t > s.k0 || h > 0 || kk > 0) ? 1u : 0u);
+                        tc_commit(bar(Sh::kVEmpty + vs));
+                        if (++vs == Sh::kVStages) {
+                            vs = 0;
+                            ++vround;
+                        }
+                    }
+                    tc_commit(bar(Sh::kODone));
+                }
+                if (!ok)
+                    break;
+                ++u;
+                s = nx;
+                has = has_nx;
+                has_nx = has && next_part(&nx, true);
+            }
+            if (!ok)
+                raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+            tc_commit(bar(Sh::kDrain));
+            mbar_wait_tries(bar(Sh::kDrain), 0u);
+        }
+    } else if constexpr (TR) {
+        // ---- TR: softmax, thread = key of the tile = TMEM lane; output, thread
+        // = column of the head = TMEM lane.  Query row c is TMEM column c. ----
+        const int key = warp * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const float sc = a.scale_log2;
+        const bool fold = sc > 0.f;
+        const float sm = fold ? 1.f : sc, se = fold ? sc : 1.f;
+        uint8_t *sp = data + Sh::kPOff;
+        // B[k][n] of the sums' products, k = row parity within 8 (+ 8: next register
+        // but one), n = lane / 4: outputs 0 .. 3 of even groups, 4 .. 7 of odd ones
+        constexpr float kMove = 14.f;                // weights stay below 2^14: they fit fp16, and bf16 however large V is
+        const uint32_t one = BF16 ? 0x3f80u : 0x3c00u;
+        const uint32_t pick = (lane & 4) ? one << 16 : one;
+        uint32_t ones0[2], ones1[2];
+        ones0[0] = (lane >> 3) == 0 ? pick : 0u, ones0[1] = (lane >> 3) == 1 ? pick : 0u;
+        ones1[0] = (lane >> 3) == 2 ? pick : 0u, ones1[1] = (lane >> 3) == 3 ? pick : 0u;
+        float *scratch = reinterpret_cast<float *>(sp);      // while no P V runs: [4][64], [64]
+        bool ok = true;
+        int J = 0, scans = 0, shares_ = 0, votes = 0, u = 0;
+        // exchange between the four warps through shared memory written before
+        auto all_four = [&](int b, int &count) -> bool {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(b));
+            const bool got = mbar_wait_tries(bar(b), (uint32_t)(count & 1));
+            ++count;
+            return __all_sync(0xffffffffu, got);
+        };
+        for (; ok; ++u) {
+            const int slot = u % kTreeParts;
+            ok = __all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kPartFull + slot), (uint32_t)((u / kTreeParts) & 1)));
+            const volatile TreePart &s = s_part[slot];
+            const int k0 = s.k0, k1 = s.k1;
+            if (!ok || k1 == 0)
+                break;
+            const int rows = s.n * G;                    // <= 64
+            const int chunks = rows > 32 ? 2 : 1;
+            const int first_masked = (s.len - s.n) / KEYS;
+            float m_own[2] = {kNegInf, kNegInf};     // maxima of rows lane and lane + 32
+            // sums[q][e]: row 16 q + 4 (lane & 3) + e, over the keys 4 (lane >> 2) .. + 3 of the warp's 32
+            float sums[4][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sums[i >> 2][i & 3] = 0.f;
+            bool was_masked = false;
+            auto mend = [&](int t) -> bool {
+                const bool bad = was_masked && *reinterpret_cast<volatile uint32_t *>(&loc->bad[(scans - 1) % kTreeScans]);
+                if (bad) {
+                    tree_add_nonfinite_t<BS, BF16>(a.value_cache, a.block_tables + (size_t)s.b * a.max_blocks, a.num_blocks,
+                                                   a.num_kv_heads, s.kvh, a.tree_mask + (size_t)s.q0 * a.words, a.words, G, s.n,
+                                                   s.len, t, key, tO + lane_base);
+                    __syncwarp();
+                }
+                return bad;
+            };
+            for (int t = k0; t < k1; ++t, ++J) {
+                const int sb = J & 1;
+                const bool masked = t >= first_masked;
+                uint64_t vis = ~0ull;                    // the rows that see this thread's key
+                if (masked)
+                    vis = tree_rows_that_see<BS, 8>(a.tree_mask + (size_t)s.q0 * a.words, a.words, G, s.n, s.len, t * KEYS + key / BS * BS,
+                                                 key % BS);
+                ok = __all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kSFull + sb), (uint32_t)((J >> 1) & 1)));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint64_t se2 = f2(se, se);
+                uint32_t pk[2][16];
+                float over[2] = {kNegInf, kNegInf};      // how far a score lies above its row's maximum
+                // weights of 32 rows against the maxima in loc->m
+                auto weigh = [&](int cc) {
+                    uint32_t raw[32];
+                    tmem_ld32(tmem + lane_base + sb * 64 + cc * 32, raw);
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = __uint_as_float(raw[i]);
+                    if (!fold) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] *= sm;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(loc->m + cc * 32 + i);
+                        const uint64_t lo = fma2(f2(x[i], x[i + 1]), se2, f2(-m.x, -m.y));
+                        const uint64_t hi = fma2(f2(x[i + 2], x[i + 3]), se2, f2(-m.z, -m.w));
+                        x[i] = f2_lo(lo);
+                        x[i + 1] = f2_hi(lo);
+                        x[i + 2] = f2_lo(hi);
+                        x[i + 3] = f2_hi(hi);
+                    }
+                    if (masked) {
+                        const uint32_t w = (uint32_t)(vis >> (cc * 32));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = (w >> i) & 1u ? x[i] : kNegInf;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        over[0] = fmax3_nan(over[0], x[i], x[i + 1]);
+                        over[1] = fmax3_nan(over[1], x[i + 2], x[i + 3]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        pk[cc][i] = pack2<BF16>(ex2(x[2 * i]), ex2(x[2 * i + 1]));
+                };
+                // A part's first maxima: the scores of its first key, if every row
+                // sees it (not above the true ones, and seldom far below them);
+                // infinities and NaN there are voted out.
+                const bool lead = t == k0 && !masked;
+                if (lead) {
+                    if (warp == 0) {
+#pragma unroll 1
+                        for (int cc = 0; cc < chunks; ++cc) {
+                            uint32_t raw[32];
+                            tmem_ld32(tmem + lane_base + sb * 64 + cc * 32, raw);
+                            if (lane == 0) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    loc->m[cc * 32 + i] = __uint_as_float(raw[i]) * sc;
+                            }
+                        }
+                    }
+                    if (!(ok = all_four(Sh::kShare, shares_)))
+                        break;
+                    m_own[0] = loc->m[lane];
+                    m_own[1] = loc->m[lane + 32];
+                }
+                bool move = t == k0 && !lead, weighed = false;
+                if (!move) {
+                    weigh(0);
+                    if (chunks > 1)
+                        weigh(1);
+                    const bool v = __any_sync(0xffffffffu, !(fmax3_nan(over[0], over[1], kNegInf) <= kMove));
+                    if (lane == 0)
+                        loc->vote[sb][warp] = v;
+                    // the maxima are the CTA's: any warp's vote moves them
+                    if (!(ok = all_four(Sh::kVote, votes)))
+                        break;
+                    const volatile uint32_t *vt = loc->vote[sb];
+                    move = (vt[0] | vt[1] | vt[2] | vt[3]) != 0u;
+                    weighed = !move;
+                }
+                if (t > k0) {
+                    // P_{J-1} V_{J-1} has completed: the weights' buffer is free, O stable
+                    ok = __all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kODone), (uint32_t)((J - 1) & 1)));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    weighed = !mend(t - 1) && weighed;       // (the weights do not outlive its call)
+                }
+                if (move) {
+                    // The rows' maxima over this tile: per warp by exchanges in which
+                    // a lane keeps one row, then over the warps.
+#pragma unroll 1
+                    for (int cc = 0; cc < chunks; ++cc) {
+                        uint32_t raw[32];
+                        tmem_ld32(tmem + lane_base + sb * 64 + cc * 32, raw);
+                        const uint32_t w = (uint32_t)(vis >> (cc * 32));
+                        float x[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float v = __uint_as_float(raw[i]) * sc;
+                            x[i] = (w >> i) & 1u ? v : kNegInf;
+                        }
+#pragma unroll
+                        for (int k = 16; k; k >>= 1) {
+                            const bool up = (lane & k) != 0;
+#pragma unroll
+                            for (int i = 0; i < k; ++i) {
+                                const float send = up ? x[i] : x[i + k], stay = up ? x[i + k] : x[i];
+                                x[i] = fmaxf(stay, __shfl_xor_sync(0xffffffffu, send, k));
+                            }
+                        }
+                        scratch[warp * 64 + cc * 32 + lane] = x[0];
+                    }
+                    if (!(ok = all_four(Sh::kShare, shares_)))
+                        break;
+                    float *s_alpha = scratch + 256;
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        if (cc >= chunks)
+                            break;
+                        const int c = cc * 32 + lane;
+                        float M = fmaxf(fmaxf(scratch[c], scratch[64 + c]), fmaxf(scratch[128 + c], scratch[192 + c]));
+                        if (lead)
+                            m_own[cc] = kNegInf;
+                        M = M > m_own[cc] + kMove ? M : m_own[cc];
+                        const float alpha = M == m_own[cc] ? 1.f : ex2(m_own[cc] - M);
+                        m_own[cc] = M;
+                        // (every warp writes the same values)
+                        loc->m[c] = M == kNegInf ? 0.f : M;
+                        s_alpha[c] = alpha;
+                    }
+                    __syncwarp();
+                    if (t > k0) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                sums[q][e] *= s_alpha[16 * q + 4 * (lane & 3) + e];   // (past the rows: 0, or not used)
+#pragma unroll 1
+                        for (int cc = 0; cc < chunks; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + lane_base + cc * 32, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * s_alpha[cc * 32 + i]);
+                            tmem_st32(tO + lane_base + cc * 32, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    // the scratch is the weights' buffer: all have read it
+                    if (!(ok = all_four(Sh::kShare, shares_)))
+                        break;
+                }
+                if (!weighed) {
+                    weigh(0);
+                    if (chunks > 1)
+                        weigh(1);
+                }
+                // P^T: key's row of 64 query rows, 128-byte swizzle
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc)
+                    if (cc < chunks) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            *reinterpret_cast<uint4 *>(sp + key * 128 + (((cc * 4 + v) ^ (key & 7)) << 4)) =
+                                make_uint4(pk[cc][4 * v], pk[cc][4 * v + 1], pk[cc][4 * v + 2], pk[cc][4 * v + 3]);
+                    }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(Sh::kPFull));
+                // The rows' sums, of the rounded weights that the products take: a
+                // register holds a key (the lane's) of two rows, which as A of an
+                // mma is 4 keys x 2 rows along k; B's ones (b0, b1) keep the rows apart.
+                // A NaN weight would reach the others of its product and is left
+                // out: its row's O is NaN whatever the sum.
+                const bool nan = __any_sync(0xffffffffu, over[0] != over[0] || over[1] != over[1]);
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                    if (g < 4 * chunks) {
+                        const uint32_t *p = &pk[g >> 2][4 * (g & 3)];
+                        uint32_t A[4] = {p[0], p[1], p[2], p[3]};
+                        if (nan) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                A[e] &= ~(nonfinite2<BF16>(A[e]) * 0xffffu);
+                        }
+                        mma_16816<BF16>(sums[g >> 1], A, g & 1 ? ones1[0] : ones0[0], g & 1 ? ones1[1] : ones0[1]);
+                    }
+                was_masked = masked;
+                scans += masked ? 1 : 0;
+            }
+            if (!ok)
+                break;
+            ok = __all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kODone), (uint32_t)((J - 1) & 1)));
+            if (!ok)
+                break;
+            tc_fence_after();
+            mend(k1 - 1);
+            // the rows' sums over the four warps
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = sums[q][e];
+                    v += __shfl_xor_sync(0xffffffffu, v, 4);
+                    v += __shfl_xor_sync(0xffffffffu, v, 8);
+                    v += __shfl_xor_sync(0xffffffffu, v, 16);
+                    if (lane < 4)
+                        scratch[warp * 64 + 16 * q + 4 * lane + e] = v;
+                }
+            if (!(ok = all_four(Sh::kShare, shares_)))
+                break;
+            const bool item = k0 == 0 && k1 == s.tiles;
+            float l_own[2];
+            float *s_inv = scratch + 256 + warp * 64;    // each warp's own copy
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                const int c = cc * 32 + lane;
+                const float l = (scratch[c] + scratch[64 + c]) + (scratch[128 + c] + scratch[192 + c]);
+                l_own[cc] = l;
+                s_inv[c] = l == 0.f ? 0.f : __frcp_rn(l);
+            }
+            __syncwarp();
+            const uint32_t div_g = (65536u + G - 1) / G;     // c / G = c div_g >> 16 (c < 64)
+#pragma unroll 1
+            for (int cc = 0; cc < chunks; ++cc) {
+                uint32_t o[32];
+                tmem_ld32(tO + lane_base + cc * 32, o);
+                const int cnt = min(32, rows - cc * 32);
+                if (item) {
+                    // row by row: token cc * 32 / G, then on by heads and tokens
+                    const uint32_t c0 = cc * 32, tok = c0 * div_g >> 16;
+                    int left = (int)(G - (c0 - tok * G));            // rows left of the token
+                    uint16_t *at = a.out + ((size_t)(s.q0 + (int)tok) * a.num_heads + (size_t)s.kvh * G + (c0 - tok * G)) * D + key;
+                    const size_t hop = (size_t)(a.num_heads - G) * D;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < cnt) {
+                            *at = to_storage<BF16>(__uint_as_float(o[i]) * s_inv[c0 + i]);
+                            at += D;
+                            if (--left == 0) {
+                                at += hop;
+                                left = G;
+                            }
+                        }
+                } else {
+                    const size_t rec = (((size_t)blockIdx.x * 2 + s.share) * 2 + (k0 > 0 ? 0 : 1)) * kTreeRows + cc * 32;
+                    float *orec = a.rec_o + rec * D + key;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < cnt)
+                            orec[(size_t)i * D] = __uint_as_float(o[i]);
+                    if (warp == 0 && lane < cnt)
+                        a.rec_ml[rec + lane] = make_float2(m_own[cc], l_own[cc]);
+                }
+            }
+            // the scratch becomes weights again: all have read it
+            if (!(ok = all_four(Sh::kShare, shares_)))
+                break;
+            if (lane == 0)
+                mbar_arrive(bar(Sh::kPartEmpty + slot));
+        }
+        if (!ok && lane == 0)
+            raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
     } else {
         // ---- softmax and epilogue: thread = row r of the tile = TMEM lane r ----
         const int r = warp * 32 + lane;
@@ -994,8 +1522,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // The part's fields stay in its slot of the queue, which this warp
             // gives back when it is done: the key loop needs the registers.
             const int slot = u % kTreeParts;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(Sh::kPartFull + slot), (uint32_t)((u / kTreeParts) & 1),
-                                                           kWaitLimitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait_tries(bar(Sh::kPartFull + slot), (uint32_t)((u / kTreeParts) & 1)));
             const volatile TreePart &s = s_part[slot];
             const int k1 = s.k1;
             if (!ok || k1 == 0)
@@ -1032,7 +1559,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         vis_now = (vis_now & low) | ((vis_now & ~low) << (BS - tail));
                     }
                 }
-                ok = mbar_wait_bounded(bar(Sh::kSFull + sb), (uint32_t)((J >> 1) & 1), kWaitLimitNs);
+                ok = mbar_wait_tries(bar(Sh::kSFull + sb), (uint32_t)((J >> 1) & 1));
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -1040,54 +1567,81 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc_fence_after();
                 bool resc = false;
                 float alpha = 1.f;
-                uint32_t pk[32];
                 if (warp_on) {
-                    uint32_t raw[64];
-                    tmem_ld64(tmem + lane_base + sb * kTreeKeys, raw);
-                    float x[64];
+                    // 32 keys at a time, by loops that are not unrolled: once for the
+                    // maximum, once for the weights, which take the place of the scores
+                    const uint32_t ts = tmem + lane_base + sb * kTreeKeys;
+                    const uint32_t vis2[2] = {(uint32_t)vis_now, (uint32_t)(vis_now >> 32)};
+                    float x[32];
+                    auto scores = [&](int h) {
+                        uint32_t raw[32];
+                        tmem_ld32(ts + h * 32, raw);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        x[c] = __uint_as_float(raw[c]);
-                    if (!fold) {
+                        for (int c = 0; c < 32; ++c)
+                            x[c] = __uint_as_float(raw[c]);
+                        if (!fold) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            x[c] *= sm;
+                            for (int c = 0; c < 32; ++c)
+                                x[c] *= sm;
+                        }
+                        if (masked) {
+                            const uint32_t w = h ? vis2[1] : vis2[0];
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                x[c] = ((w >> c) & 1u) ? x[c] : kNegInf;
+                        }
+                    };
+                    float mt;
+                    {
+                        uint32_t raw[64];
+                        tmem_ld64(ts, raw);
+                        if (!fold) {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                raw[c] = __float_as_uint(__uint_as_float(raw[c]) * sm);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                raw[c] = (vis2[c >> 5] >> (c & 31)) & 1u ? raw[c] : 0xff800000u;
+                        }
+                        float mx[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mx[i] = fmaxf(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
+#pragma unroll
+                        for (int c = 16; c < 64; c += 2)
+                            mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(raw[c]), __uint_as_float(raw[c + 1]));
+                        mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
                     }
-                    if (masked) {
-                        const uint32_t vlo = (uint32_t)vis_now, vhi = (uint32_t)(vis_now >> 32);
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            x[c] = (((c < 32 ? vlo : vhi) >> (c & 31)) & 1u) ? x[c] : kNegInf;
-                    }
-                    float mx[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mx[i] = fmaxf(x[2 * i], x[2 * i + 1]);
-#pragma unroll
-                    for (int c = 16; c < 64; c += 2)
-                        mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], x[c], x[c + 1]);
-                    const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * se;
+                    mt *= se;
                     resc = real && mt > m_used + 8.f;
                     const float m_new = resc ? mt : m_used;
                     alpha = resc ? ex2(m_used - m_new) : 1.f;
                     const float msub = m_new == kNegInf ? 0.f : m_new;
                     // the row sum is taken over the rounded weights the MMA multiplies
                     const uint64_t se2 = f2(se, se), nm2 = f2(-msub, -msub);
-                    uint64_t rsv[4] = {0ull, 0ull, 0ull, 0ull};
+                    uint64_t rsv[2] = {0ull, 0ull};
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        scores(h);
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const uint64_t e = fma2(f2(x[2 * c], x[2 * c + 1]), se2, nm2);
-                        pk[c] = pack2<BF16>(ex2(f2_lo(e)), ex2(f2_hi(e)));
-                        const float2 pr = unpack2<BF16>(pk[c]);
-                        rsv[c & 3] = add2(rsv[c & 3], f2(pr.x, pr.y));
+                        for (int c = 0; c < 16; ++c) {
+                            const uint64_t e = fma2(f2(x[2 * c], x[2 * c + 1]), se2, nm2);
+                            pk[c] = pack2<BF16>(ex2(f2_lo(e)), ex2(f2_hi(e)));
+                            const float2 pr = unpack2<BF16>(pk[c]);
+                            rsv[c & 1] = add2(rsv[c & 1], f2(pr.x, pr.y));
+                        }
+                        tmem_st16(ts + h * 16, pk);
                     }
-                    const uint64_t r2 = add2(add2(rsv[0], rsv[1]), add2(rsv[2], rsv[3]));
+                    const uint64_t r2 = add2(rsv[0], rsv[1]);
                     l = l * alpha + (f2_lo(r2) + f2_hi(r2));
                     m_used = m_new;
                 }
                 if (t > k0) {
                     // P_{J-1} V_{J-1} has completed: O is stable, and O_DONE within one phase
-                    ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
+                    ok = mbar_wait_tries(bar(Sh::kODone), (uint32_t)((J - 1) & 1));
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -1106,10 +1660,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                     }
                 }
-                if (warp_on) {
-                    tmem_st32(tmem + lane_base + sb * kTreeKeys, pk);
+                if (warp_on)
                     tmem_wait_st();
-                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -1123,7 +1675,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const bool item = k0 == 0 && k1 == s.tiles;
             const size_t orow = (size_t)(s.q0 + s.rt * TT + r_tok) * a.num_heads + (size_t)s.kvh * G + r_head;
             const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-            ok = mbar_wait_bounded(bar(Sh::kODone), (uint32_t)((J - 1) & 1), kWaitLimitNs);
+            ok = mbar_wait_tries(bar(Sh::kODone), (uint32_t)((J - 1) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (ok && warp_on) {
                 tc_fence_after();
@@ -1274,75 +1826,76 @@ tree_merge_kernel(const TreeArgs a)
     asm volatile("griddepcontrol.launch_dependents;");
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int share = 0; share < a.shares; ++share) {
-    const int4 d = __ldg(a.desc + c * 2 + share);
-    const int step = a.shares == 2 && share == 0 ? 2 : 1;
-    for (int r0 = ((int)blockIdx.y * 8 + warp) * 2; r0 < d.y; r0 += (int)gridDim.y * 16) {   // (no records: d.y is 0)
-    // record k: CTA c + (k - 1) step; part 1 of the first, part 0 of the others
-    auto rec = [&](int k) {
-        return (((size_t)(c + (k - 1) * step) * 2 + share) * 2 + (k == 0 ? 1 : 0)) * kTreeRows + r0;
-    };
-    const int second = r0 + 1 < d.y ? 1 : 0;      // (an odd last row is taken twice)
-    float M[2] = {kNegInf, kNegInf};
-    for (int k = lane; k < d.w; k += 32) {
-        M[0] = fmaxf(M[0], __ldg(&a.rec_ml[rec(k)].x));
-        M[1] = fmaxf(M[1], __ldg(&a.rec_ml[rec(k) + second].x));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        M[0] = fmaxf(M[0], __shfl_xor_sync(0xffffffffu, M[0], o));
-        M[1] = fmaxf(M[1], __shfl_xor_sync(0xffffffffu, M[1], o));
-    }
-    float den[2] = {0.f, 0.f}, acc[2][V];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        acc[0][i] = acc[1][i] = 0.f;
-    auto batch = [&](auto count, int k0) {           // records k0 .. k0 + N - 1
-        constexpr int N = decltype(count)::value;
-        float2 ml[N][2];
-        float v[N][2][V];
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const size_t at = rec(k0 + j) + (q ? second : 0);
-                ml[j][q] = __ldg(a.rec_ml + at);
-                load_slice<D>(a.rec_o + at * D + lane * V, v[j][q]);
+        const int4 d = __ldg(a.desc + c * 2 + share);
+        const int step = a.shares == 2 && share == 0 ? 2 : 1;
+        for (int r0 = ((int)blockIdx.y * 8 + warp) * 2; r0 < d.y; r0 += (int)gridDim.y * 16) {   // (no records: d.y is 0)
+            // record k: CTA c + (k - 1) step; part 1 of the first, part 0 of the others
+            auto rec = [&](int k) {
+                return (((size_t)(c + (k - 1) * step) * 2 + share) * 2 + (k == 0 ? 1 : 0)) * kTreeRows + r0;
+            };
+            const int second = r0 + 1 < d.y ? 1 : 0;      // (an odd last row is taken twice)
+            float M[2] = {kNegInf, kNegInf};
+            for (int k = lane; k < d.w; k += 32) {
+                M[0] = fmaxf(M[0], __ldg(&a.rec_ml[rec(k)].x));
+                M[1] = fmaxf(M[1], __ldg(&a.rec_ml[rec(k) + second].x));
             }
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+            for (int o = 16; o; o >>= 1) {
+                M[0] = fmaxf(M[0], __shfl_xor_sync(0xffffffffu, M[0], o));
+                M[1] = fmaxf(M[1], __shfl_xor_sync(0xffffffffu, M[1], o));
+            }
+            float den[2] = {0.f, 0.f}, acc[2][V];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                acc[0][i] = acc[1][i] = 0.f;
+            auto batch = [&](auto count, int k0) {           // records k0 .. k0 + N - 1
+                constexpr int N = decltype(count)::value;
+                float2 ml[N][2];
+                float v[N][2][V];
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const size_t at = rec(k0 + j) + (q ? second : 0);
+                        ml[j][q] = __ldg(a.rec_ml + at);
+                        load_slice<D>(a.rec_o + at * D + lane * V, v[j][q]);
+                    }
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        // (1: a part without keys, or all NaN)
+                        const float f = ml[j][q].x == kNegInf ? 1.f : ex2(ml[j][q].x - M[q]);
+                        den[q] += f * ml[j][q].y;
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            acc[q][i] += f * v[j][q][i];
+                    }
+            };
+            int k0 = 0;
+            for (; k0 + 4 <= d.w; k0 += 4)
+                batch(std::integral_constant<int, 4>{}, k0);
+            if (d.w - k0 == 3)
+                batch(std::integral_constant<int, 3>{}, k0);
+            else if (d.w - k0 == 2)
+                batch(std::integral_constant<int, 2>{}, k0);
+            else if (d.w - k0 == 1)
+                batch(std::integral_constant<int, 1>{}, k0);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                // (1: a part without keys, or all NaN)
-                const float f = ml[j][q].x == kNegInf ? 1.f : ex2(ml[j][q].x - M[q]);
-                den[q] += f * ml[j][q].y;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    acc[q][i] += f * v[j][q][i];
+                const int r = r0 + q;
+                if (r >= d.y)
+                    break;
+                const float inv = den[q] == 0.f ? 0.f : 1.f / den[q];
+                uint16_t *o = a.out + ((size_t)(d.x + r / a.group) * a.num_heads + (size_t)d.z * a.group + r % a.group) * D +
+                              lane * V;
+                if constexpr (V == 4)
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv),
+                                                               pack2<BF16>(acc[q][2] * inv, acc[q][3] * inv));
+                else
+                    *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv);
             }
-    };
-    int k0 = 0;
-    for (; k0 + 4 <= d.w; k0 += 4)
-        batch(std::integral_constant<int, 4>{}, k0);
-    if (d.w - k0 == 3)
-        batch(std::integral_constant<int, 3>{}, k0);
-    else if (d.w - k0 == 2)
-        batch(std::integral_constant<int, 2>{}, k0);
-    else if (d.w - k0 == 1)
-        batch(std::integral_constant<int, 1>{}, k0);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int r = r0 + q;
-        if (r >= d.y)
-            break;
-        const float inv = den[q] == 0.f ? 0.f : 1.f / den[q];
-        uint16_t *o = a.out + ((size_t)(d.x + r / a.group) * a.num_heads + (size_t)d.z * a.group + r % a.group) * D + lane * V;
-        if constexpr (V == 4)
-            *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv),
-                                                       pack2<BF16>(acc[q][2] * inv, acc[q][3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[q][0] * inv, acc[q][1] * inv);
-    }
-    }
+        }
     }
 }
 
@@ -1359,11 +1912,11 @@ tree_merge_kernel(const TreeArgs a)
 // by V, so the weights keep about 16 bits more.  A CTA takes part_tokens keys
 // of a (sequence, kv head), a warp every other page of them.  An item of one
 // part is written out, of several as records that tree_rows_merge_kernel joins.
-// Bound by the cache's bytes: batches of 256 x 576 tokens, 8 kv heads of 128, 2
-// nodes x 4 heads take 110 us (0.89 of the measured copy rate; the 128-row
-// tiles take 132), 40 heads of one node row each more than 1.0 of it.  With 32
-// rows the legacy matrix instructions bound it (174 us against 138), so more
-// rows go to the tiles above.
+// Bound by the cache's bytes: 256 x 512 .. 640 tokens, 8 kv heads of 128, 2
+// nodes x 4 heads take 107 us, 4 nodes 112 (0.86 of the measured copy rate;
+// the 128-row tiles 110 and 120, sustained 130 and 131 against 107 and 111).
+// With 32 rows the legacy matrix instructions bound it (174 us against 117), so
+// more rows go to the tiles above.
 struct TreeRowsArgs {
     const uint16_t *query;           // [T, Hq, D]
     const int32_t *query_start;      // [batch + 1]
@@ -1501,7 +2054,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             acc[d][i] = 0.f;
     for (int k = 0; k < nk; ++k) {
         const int st = k % S;
-        const bool got = mbar_wait_bounded(full0 + 8u * st, (uint32_t)((k / S) & 1), kWaitLimitNs);
+        const bool got = mbar_wait_tries(full0 + 8u * st, (uint32_t)((k / S) & 1));
         if (!__all_sync(0xffffffffu, got)) {
             if (lane == 0)
                 raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
@@ -1665,7 +2218,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     // a wait gave up: copies in flight land (bounded) before the memory is reused
     for (int k = consumed; k < issued; ++k)
-        mbar_wait_bounded(full0 + 8u * (k % S), (uint32_t)((k / S) & 1), kWaitLimitNs / 8);
+        mbar_wait_tries(full0 + 8u * (k % S), (uint32_t)((k / S) & 1));
 
     // ---- merge the warps by log-sum-exp through shared memory ----
     __syncthreads();

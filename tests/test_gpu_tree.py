@@ -350,6 +350,84 @@ def test_attend_nonfinite_cells_in_every_kernel(heads, columns):
                 assert row[:, :6].isfinite().all() and row[:, 7:70].isfinite().all() and row[:, 71:].isfinite().all()
 
 
+# 17 to 64 query rows per item and head_dim 128 over a wide table: the kernel
+# with keys as the rows of its products.
+@pytest.mark.parametrize("Hq,Hkv,nodes", [(8, 2, [16, 3, 0, 9, 1]), (1, 1, [64, 33, 1, 17, 2]), (5, 1, [12, 1, 5, 0, 7]),
+                                          (6, 2, [21, 7, 10, 1, 0]), (8, 1, [5, 8, 1, 3, 4]), (4, 1, [8, 5, 7, 1, 2])])
+@pytest.mark.parametrize("dtype,bs", [("f16", 16), ("bf16", 32)])
+def test_attend_up_to_64_rows_planned_for_long_contexts(Hq, Hkv, nodes, dtype, bs):
+    for k, bases in enumerate(([127, 1300, 9, 0, 128], [0, 64, 50, 3001, 119], [63, 0, 700, 255, 1])):
+        c = tu.tree_case(nodes, bases, Hq, Hkv, 128, bs, dtype, seed=50 + k, columns=_WIDE[bs])
+        d = _cuda(c)
+        out = _attend(d)
+        _check(c, out)
+        for _ in range(3):
+            assert torch.equal(_attend(d), out)
+
+
+@pytest.mark.parametrize("n,base", [(9, 0), (16, 0), (16, 111), (16, 112), (16, 113), (15, 113), (13, 300), (16, 240), (10, 64)])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_attend_borders_up_to_64_rows(n, base, bs):
+    c = tu.tree_case([n], [base], 4, 1, 128, bs, "bf16", seed=n * 1000 + base, columns=_WIDE[bs])
+    _check(c, _attend(_cuda(c)))
+
+
+def test_attend_any_bits_up_to_64_rows():
+    g = torch.Generator().manual_seed(51)
+    nodes, bases = [40, 6, 64, 3], [0, 0, 100, 20]
+    bits = [(torch.rand(n, 64, generator=g) < 0.3).numpy() for n in nodes]
+    for x, n in zip(bits, nodes):
+        x[n // 2] = False
+        x[n // 2, n:] = True
+    c = tu.tree_case(nodes, bases, 2, 2, 128, 16, "f16", seed=52, bits=bits, max_query_len=64, columns=_WIDE[16])
+    out = _attend(_cuda(c))
+    _check(c, out)
+    assert (out[20] == 0).all() and (out[43] == 0).all()
+
+
+@pytest.mark.parametrize("columns", [0, 4096])
+@pytest.mark.parametrize("nodes", [[4, 3], [12, 16], [12, 30]])
+def test_attend_moving_maxima_in_every_kernel(columns, nodes):
+    # scores that grow along the keys, that fall, and one early key far above or below the others
+    for shape in ("grow", "fall", "high", "low"):
+        c = tu.tree_case(nodes, [500, 700], 8, 2, 128, 16, "bf16", seed=53, q_scale=30.0, columns=columns)
+        for k in c["keys"]:
+            n = k.shape[0]
+            f = torch.arange(n) / n * 3 + 0.2
+            if shape == "fall":
+                f = f.flip(0)
+            if shape in ("high", "low"):
+                f = torch.full((n,), 0.05)
+                f[0 if shape == "low" else 150] = 4.0
+            k *= f[:, None, None].to(k.dtype)
+        for b, k in enumerate(c["keys"]):
+            for j in range(k.shape[0]):
+                c["key_cache"][int(c["block_tables"][b, j // 16]), j % 16] = k[j]
+        _check(c, _attend(_cuda(c)))
+
+
+@pytest.mark.parametrize("heads", [(4, 2), (16, 2)])
+@pytest.mark.parametrize("columns", [0, 4096])
+@pytest.mark.parametrize("nodes", [[2, 1], [7, 4], [25, 13]])
+def test_attend_nan_query_row_stays_its_own(heads, columns, nodes):
+    c = tu.tree_case(nodes, [300, 20], *heads, 128, 16, "f16", seed=54, columns=columns)
+    d = _cuda(c)
+    d["query"][1, 1, 17] = float("nan")
+    out = _attend(d)
+    assert out[1, 1].isnan().all()
+    ref, tol = tu.attend_reference(c)
+    fine = torch.ones(sum(nodes), heads[0], dtype=torch.bool)
+    fine[1, 1] = False
+    assert ((out.double().cpu() - ref).abs() <= tol)[fine].all()
+
+
+def test_attend_negative_zero_and_tiny_scale_up_to_64_rows():
+    for scale in (-0.3, 0.0, 1e-6):
+        c = tu.tree_case([20, 5], [300, 0], 4, 2, 128, 16, "bf16", seed=55, columns=_WIDE[16])
+        c["scale"] = scale
+        _check(c, _attend(_cuda(c)))
+
+
 def test_attend_many_short_sequences():
     # more sequences than a CTA has threads, some without rows; shares hold many small items
     g = torch.Generator().manual_seed(27)

@@ -102,7 +102,9 @@ def attend_reference(c):
     output once more (h |out|), and works in 32 bits elsewhere:
       weights    h * sum_j p_j |v_j - out|
       output     h * |out|
-      scores     a sum of D products has an error of at most D 2^-24 sum_d |q_d k_d|;
+      scores     a sum of D products has an error of at most D 2^-24 sum_d |q_d k_d|,
+                 times |scale| (an error has no sign: with a negative scale the signed
+                 factor took 2 d off the bound instead of adding it);
                  an error d in a score changes its weight by d relative, its share
                  and the normaliser by as much again: 2 d sum_j p_j |v_j|; 2^-20
                  covers the exponent's argument and the exponential itself
@@ -131,7 +133,7 @@ def attend_reference(c):
                 w = torch.exp(x - x.max())
                 p = w / w.sum()
                 o = p @ vv
-                d = D * 2.0 ** -24 * c["scale"] * float((kk.abs() @ q.abs()).max())
+                d = D * 2.0 ** -24 * abs(c["scale"]) * float((kk.abs() @ q.abs()).max())
                 absv = p @ vv.abs()
                 t = h * o.abs() + h * (p @ (vv - o).abs()) + (2 * d + 2.0 ** -20 + (L / 16 + 16) * 2.0 ** -23) * absv
                 if c["dtype"] == "f16":
