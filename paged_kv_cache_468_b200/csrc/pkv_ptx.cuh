@@ -81,7 +81,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 // The same, bounded by a number of tries: one that fails takes 4 us, so 2^19 of
 // them about 2 s.  Half the instructions of the timed form, for kernels whose
 // warps wait at many places and run out of instruction cache (tree attention,
-// 256 sequences of 512 .. 640 tokens with 16 drafted each: 138 to 129 us).
+// 256 sequences of 512 .. 640 tokens with 12 .. 16 drafted each: 147 to 138 us).
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity)
 {
 #pragma unroll 1

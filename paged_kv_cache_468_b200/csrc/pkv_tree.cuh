@@ -279,7 +279,7 @@ struct TreeArgs {
 constexpr int kTreeThreads = 256;
 constexpr int kTreeRows = 128;           // query rows per tile (MMA M)
 constexpr int kTreeKeys = 64;            // keys per tile
-constexpr int kTreeItemCost = 3;         // an item's start and end, in key tiles
+constexpr int kTreeItemCost = 2;         // an item's start and end, in key tiles (1 to 5: within 4 %, 1 and 2 ahead)
 constexpr int kTreeMinUnits = 2;         // a CTA's share is not cut below this
 
 constexpr int kTreeParts = 6;            // queue of parts between a CTA's warps
