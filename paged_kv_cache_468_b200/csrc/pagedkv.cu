@@ -1438,8 +1438,9 @@ extern "C" pkv_status pkv_paged_attention_tree(
     if (num_blocks <= 0 || num_blocks * block_size >= ((int64_t)1 << 31))
         return fail(PKV_ERR_INVALID_ARG, "num_blocks %lld: need 0 < num_blocks*block_size < 2^31",
                     (long long)num_blocks);
-    if (!std::isfinite(scale))
-        return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (!std::isfinite(scale_log2))
+        return fail(PKV_ERR_INVALID_ARG, "scale x log2(e) is not finite");
     if (batch == 0 || max_query_len == 0 || num_tokens == 0)
         return PKV_OK;
     if (!query || !query_start || !tree_mask || !key_cache || !value_cache || !block_tables ||
@@ -1461,7 +1462,6 @@ extern "C" pkv_status pkv_paged_attention_tree(
     const int group = num_heads / num_kv_heads;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
     if (plan.few) {
         CUtensorMap mk, mv;
         if ((s = make_cache_map(&mk, key_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)) != PKV_OK ||

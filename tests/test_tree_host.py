@@ -59,6 +59,7 @@ def test_tree_attention_host_validation():
     assert call(nb=0) == pagedkv.ERR_INVALID_ARG
     assert call(nb=1 << 27) == pagedkv.ERR_INVALID_ARG             # num_blocks * block_size = 2^31
     assert call(scale=float("nan")) == pagedkv.ERR_INVALID_ARG
+    assert call(scale=3.4e38) == pagedkv.ERR_INVALID_ARG          # (times log2 e it is infinite)
     assert call(mask=None) == pagedkv.ERR_INVALID_ARG
     assert call(q=A16 + 8) == pagedkv.ERR_MISALIGNED
     assert call(mask=A16 + 2) == pagedkv.ERR_MISALIGNED
