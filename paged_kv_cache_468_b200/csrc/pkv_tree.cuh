@@ -669,8 +669,6 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 p.k1 = 0;
             loc->part[0] = p;
             loc->part[1].k1 = 0;
-            mbar_arrive(bar(Sh::kPartFull));
-            mbar_arrive(bar(Sh::kPartFull + 1));
         }
         if (P > 1 && tiles > 1) {                    // (a single tile is one CTA's alone)
             cl_tiles = tiles;
@@ -681,6 +679,11 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
+        // (behind the block's barrier: other threads initialised these two)
+        if (threadIdx.x == 0) {
+            mbar_arrive(bar(Sh::kPartFull));
+            mbar_arrive(bar(Sh::kPartFull + 1));
+        }
     }
     // ---- this CTA's shares: a thread adds up a run of sequences, the block
     // their totals; the thread whose run holds the share's start finds it ----
