@@ -524,8 +524,9 @@ pkv_status pkv_alloc_fork(pkv_alloc *a, const int32_t *blocks, int n);
  * is not a block multiple and the partly filled last block is shared
  * (refcount > 1), it is first replaced by a fresh block (copy-on-write): the
  * pair is reported as cow_src[0] -> cow_dst[0] with *n_cow = 1 so the caller
- * can copy the cells, and the shared block's refcount drops by one.  On
- * PKV_ERR_OOM nothing changes.
+ * can copy the cells, and the shared block's refcount drops by one.  A partly
+ * filled last block that is not shared is dropped from the prefix cache: its
+ * cells are about to be written.  On PKV_ERR_OOM nothing changes.
  */
 pkv_status pkv_alloc_append(pkv_alloc *a, int32_t *blocks, int capacity, int *n,
                             int64_t old_len, int64_t new_len,
@@ -539,8 +540,10 @@ pkv_status pkv_alloc_free(pkv_alloc *a, const int32_t *blocks, int n);
 /*
  * Shrink a sequence to new_len tokens: the blocks of its table behind
  * ceil(new_len / block_size) are released as by pkv_alloc_free and *n becomes
- * that number.  A table that is already as short is left as it is; new_len < 0
- * is PKV_ERR_INVALID_ARG.  On an error nothing changes.
+ * that number.  A table that is already as short keeps its blocks; new_len < 0
+ * is PKV_ERR_INVALID_ARG.  Where new_len ends inside the last block that is
+ * kept, that block is dropped from the prefix cache unless other sequences
+ * share it (append then copies it).  On an error nothing changes.
  */
 pkv_status pkv_alloc_truncate(pkv_alloc *a, const int32_t *blocks, int *n, int64_t new_len);
 

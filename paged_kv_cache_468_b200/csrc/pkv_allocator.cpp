@@ -214,6 +214,10 @@ pkv_status pkv_alloc_append(pkv_alloc *a, int32_t *blocks, int capacity, int *n,
         cow_dst[0] = dst;
         *n_cow = 1;
     }
+    // A tail that is written in place no longer holds the tokens it was
+    // registered for (it was full once and its sequence was cut short).
+    if (partial_tail && !cow)
+        uncache(a, blocks[have - 1]);
     for (int64_t i = have; i < want; ++i)
         blocks[i] = take_block(a);
     *n = (int)want;
@@ -252,14 +256,26 @@ pkv_status pkv_alloc_truncate(pkv_alloc *a, const int32_t *blocks, int *n, int64
         return err(PKV_ERR_INVALID_ARG, "truncate: bad handle, count or length");
     const int64_t bs = a->block_size;
     const int64_t keep = new_len / bs + (new_len % bs != 0);
-    if (keep >= *n)
+    if (keep > *n || *n == 0)
         return PKV_OK;
     if (!blocks)
         return err(PKV_ERR_INVALID_ARG, "truncate: no block list");
-    const pkv_status s = pkv_alloc_free(a, blocks + keep, *n - (int)keep);
-    if (s == PKV_OK)
-        *n = (int)keep;
-    return s;
+    // the block that becomes (or stays) the partly filled tail
+    const bool partial = new_len % bs != 0;
+    if (partial) {
+        const int32_t id = blocks[keep - 1];
+        if (id < 0 || (size_t)id >= a->refcount.size() || a->refcount[(size_t)id] <= 0)
+            return err(PKV_ERR_OUT_OF_RANGE, "truncate: block id outside the pool or free");
+    }
+    const pkv_status s = keep < *n ? pkv_alloc_free(a, blocks + keep, *n - (int)keep) : PKV_OK;
+    if (s != PKV_OK)
+        return s;
+    // Its cells behind new_len will hold other tokens than those it was
+    // registered for.  (A shared one stays as it is: append copies it first.)
+    if (partial && a->refcount[(size_t)blocks[keep - 1]] == 1)
+        uncache(a, blocks[keep - 1]);
+    *n = (int)keep;
+    return PKV_OK;
 }
 
 // ---- automatic prefix caching -------------------------------------------

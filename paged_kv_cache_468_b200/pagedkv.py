@@ -678,7 +678,8 @@ class BlockAllocator:
         _check(lib().pkv_alloc_free(self._h, self._arr(blocks), len(blocks)), "pkv_alloc_free")
 
     def truncate(self, blocks: list, new_len: int) -> None:
-        """Shrink a sequence's table in place to the blocks of new_len tokens; the rest is released."""
+        """Shrink a sequence's table in place to the blocks of new_len tokens; the rest is released.
+        A last block that new_len ends inside is dropped from the prefix cache unless it is shared."""
         n = ctypes.c_int(len(blocks))
         _check(lib().pkv_alloc_truncate(self._h, self._arr(blocks), ctypes.byref(n), int(new_len)),
                "pkv_alloc_truncate")
