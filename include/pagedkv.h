@@ -470,8 +470,11 @@ pkv_status pkv_draft_tree_accept(const int64_t *draft_tokens, const int64_t *tar
  * list of positions from all over a context it drops the others from the
  * cache.  The result is as if all cells were read before any is written.
  * Cells from start_lens[b] + keep_lens[b] on keep what they held.  The pages
- * that are written must belong to one sequence of the call alone (copy shared
- * pages first).  A negative start, a count outside 0 .. max_keep or a range
+ * that are written (from the first moved cell's target to the last one's) must
+ * belong to one sequence of the call alone (copy shared pages first) and must
+ * not be registered in the prefix cache, whose hashes name what they held
+ * (pkv_alloc_cache_remove first; pages of drafted tokens are not registered
+ * before they are accepted).  A negative start, a count outside 0 .. max_keep or a range
  * past the table sets PKV_DEVFLAG_CONTEXT_RANGE and the sequence is skipped;
  * kept positions that do not ascend or lie past the table set
  * PKV_DEVFLAG_INDEX_RANGE and a page id outside the pool
@@ -566,6 +569,14 @@ uint64_t pkv_block_hash(uint64_t parent_hash, const int32_t *tokens, int n);
 /* Register an in-use block (refcount > 0) under `hash`.  No-op if the block
  * is already registered or another block holds that hash. */
 pkv_status pkv_alloc_cache_insert(pkv_alloc *a, uint64_t hash, int32_t block);
+
+/*
+ * Drop blocks from the prefix cache, before cells of theirs are rewritten in
+ * place (pkv_kv_cache_compact); one that is not registered is passed over, one
+ * that no sequence uses becomes free.  PKV_ERR_OUT_OF_RANGE (nothing changed)
+ * if an id is outside the pool.
+ */
+pkv_status pkv_alloc_cache_remove(pkv_alloc *a, const int32_t *blocks, int n);
 
 /* Block registered under `hash` with its refcount raised by one (a released
  * block is revived), or -1 if none. */

@@ -317,6 +317,26 @@ pkv_status pkv_alloc_cache_insert(pkv_alloc *a, uint64_t hash, int32_t block)
     return PKV_OK;
 }
 
+pkv_status pkv_alloc_cache_remove(pkv_alloc *a, const int32_t *blocks, int n)
+{
+    if (!a || n < 0 || (n > 0 && !blocks))
+        return err(PKV_ERR_INVALID_ARG, "cache_remove: bad handle or block list");
+    for (int i = 0; i < n; ++i)
+        if (blocks[i] < 0 || (size_t)blocks[i] >= a->refcount.size())
+            return err(PKV_ERR_OUT_OF_RANGE, "cache_remove: block id outside the pool");
+    for (int i = 0; i < n; ++i) {
+        const int32_t id = blocks[i];
+        if (!a->cached[(size_t)id])
+            continue;
+        uncache(a, id);
+        if (a->refcount[(size_t)id] == 0) {       // nobody uses it and nobody can find it
+            a->evictable.erase(a->lru_pos[(size_t)id]);
+            a->free_list.push_back(id);
+        }
+    }
+    return PKV_OK;
+}
+
 int32_t pkv_alloc_cache_lookup(pkv_alloc *a, uint64_t hash)
 {
     if (!a || hash == 0)

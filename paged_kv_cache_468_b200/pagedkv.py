@@ -114,6 +114,8 @@ def lib() -> ctypes.CDLL:
                                                i32, pint, pint]
         L.pkv_alloc_truncate.restype = i32
         L.pkv_alloc_truncate.argtypes = [P, pi32, pint, i64]
+        L.pkv_alloc_cache_remove.restype = i32
+        L.pkv_alloc_cache_remove.argtypes = [P, pi32, i32]
         L.pkv_draft_tree_mask.restype = i32
         L.pkv_draft_tree_mask.argtypes = [P, i32, P, i32, P, i32, P, P, P]
         L.pkv_draft_tree_accept.restype = i32
@@ -580,7 +582,8 @@ def kv_cache_compact(key_caches, value_caches, block_tables: torch.Tensor, start
     """Move kept cells together in place (see include/pagedkv.h): cell start_lens[b] + keep[b, i] goes to
     cell start_lens[b] + i for i < keep_lens[b], in every layer.  key_caches / value_caches: the layers'
     caches [NB, bs, Hkv, D] (a list, or one tensor for one layer), block_tables int32 [B, max_blocks],
-    start_lens and keep_lens int32 [B], keep int32 [B, max_keep] ascending."""
+    start_lens and keep_lens int32 [B], keep int32 [B, max_keep] ascending.  Pages that are written must be
+    one sequence's alone and not registered in the prefix cache (BlockAllocator.cache_remove first)."""
     if isinstance(key_caches, torch.Tensor):
         key_caches, value_caches = [key_caches], [value_caches]
     if len(key_caches) != len(value_caches) or not len(key_caches):
@@ -698,6 +701,10 @@ class BlockAllocator:
     def cache_insert(self, block_hash: int, block: int) -> None:
         _check(lib().pkv_alloc_cache_insert(self._h, int(block_hash), int(block)),
                "pkv_alloc_cache_insert")
+
+    def cache_remove(self, blocks: list) -> None:
+        """Drop blocks from the prefix cache, before cells of theirs are rewritten in place."""
+        _check(lib().pkv_alloc_cache_remove(self._h, self._arr(blocks), len(blocks)), "pkv_alloc_cache_remove")
 
     def cache_lookup(self, block_hash: int) -> int:
         return int(lib().pkv_alloc_cache_lookup(self._h, int(block_hash)))
