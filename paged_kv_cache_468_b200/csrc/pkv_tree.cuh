@@ -194,8 +194,9 @@ tree_accept_kernel(const int64_t *__restrict__ draft, const int64_t *__restrict_
 //
 //   S_j = Q K_j^T,   P_j = 2^(S_j scale log2 e - m),   O += P_j V_j
 //
-// with P over S in tensor memory, S double-buffered, and the running maximum m
-// moved only when a tile exceeds it by 2^8.  Only the last key tiles of a
+// with P over S in tensor memory, S double-buffered, and the reference m (the
+// running maximum, for bf16 raised by tree_headroom) moved only when a tile's
+// maximum exceeds the one it was taken from by 2^8.  Only the last key tiles of a
 // sequence hold drafted keys: they alone are masked, by 64 bits per row cut
 // from the row's mask words.  A tile's scores are read twice, for the maximum
 // and, 32 at a time by a loop, for the weights: less code and no spills, since
@@ -390,6 +391,23 @@ __device__ __forceinline__ int tree_cut(int total, int c, int n)   // the first 
 __device__ __forceinline__ int tree_ctas(int total, int most)      // CTAs (or pairs) that share the units
 {
     return min(most, max(1, (total + kTreeMinUnits - 1) / kTreeMinUnits));
+}
+
+// How far (in powers of two) the reference that a row's weights are taken
+// against lies above the row's maximum.  The weights are summed unnormalised,
+// and reach 2^move over the maximum that they were first taken against; bf16
+// values reach 2^128, so `len` such products would overflow the 32-bit
+// accumulator where their average does not.  With the reference this much
+// higher the weights of a row add up to less than one.  bf16 has the range for
+// it, and weights that vanish now are below 2^-80 of the largest.  What it costs
+// are bits of sums of the smallest values, as 32-bit subnormals: over 1300 keys
+// the outputs are as exact as ever for values from 2^-118 (transposed: 2^-112)
+// to 2^128, and lose bits below (values of 2^-124: 0.6 %, transposed 20 %).  No
+// time.  f16 has neither such values nor the range for such weights.
+template <bool BF16>
+__device__ __forceinline__ float tree_headroom(int len, int move)
+{
+    return BF16 ? (float)(33 - __clz(len) + move) : 0.f;
 }
 
 // Row r's visible positions p0 .. p0 + 63 as bits: committed cells, and the
@@ -1191,7 +1209,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint8_t *sp = data + Sh::kPOff;
         // B[k][n] of the sums' products, k = row parity within 8 (+ 8: next register
         // but one), n = lane / 4: outputs 0 .. 3 of even groups, 4 .. 7 of odd ones
-        constexpr float kMove = 14.f;                // weights stay below 2^14: they fit fp16, and bf16 however large V is
+        constexpr float kMove = 14.f;                // f16 weights stay below 2^14 (bf16 ones below tree_headroom)
         const uint32_t one = BF16 ? 0x3f80u : 0x3c00u;
         const uint32_t pick = (lane & 4) ? one << 16 : one;
         uint32_t ones0[2], ones1[2];
@@ -1219,7 +1237,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int rows = s.n * G;                    // <= 64
             const int chunks = rows > 32 ? 2 : 1;
             const int first_masked = (s.len - s.n) / KEYS;
-            float m_own[2] = {kNegInf, kNegInf};     // maxima of rows lane and lane + 32
+            auto up = [&]() -> float { return tree_headroom<BF16>(s.len, (int)kMove); };   // (no register to keep it in)
+            float m_own[2] = {kNegInf, kNegInf};     // references (maximum + up) of rows lane and lane + 32
             // sums[q][e]: row 16 q + 4 (lane & 3) + e, over the keys 4 (lane >> 2) .. + 3 of the warp's 32
             float sums[4][4];
 #pragma unroll
@@ -1249,8 +1268,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc_fence_after();
                 const uint64_t se2 = f2(se, se);
                 uint32_t pk[2][16];
-                float over[2] = {kNegInf, kNegInf};      // how far a score lies above its row's maximum
-                // weights of 32 rows against the maxima in loc->m
+                float over[2] = {kNegInf, kNegInf};      // how far a score lies above its row's reference
+                // weights of 32 rows against the references in loc->m
                 auto weigh = [&](int cc) {
                     uint32_t raw[32];
                     tmem_ld32(tmem + lane_base + sb * 64 + cc * 32, raw);
@@ -1301,7 +1320,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (lane == 0) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    loc->m[cc * 32 + i] = __uint_as_float(raw[i]) * sc;
+                                    loc->m[cc * 32 + i] = __uint_as_float(raw[i]) * sc + up();
                             }
                         }
                     }
@@ -1315,7 +1334,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     weigh(0);
                     if (chunks > 1)
                         weigh(1);
-                    const bool v = __any_sync(0xffffffffu, !(fmax3_nan(over[0], over[1], kNegInf) <= kMove));
+                    const bool v = __any_sync(0xffffffffu, !(fmax3_nan(over[0], over[1], kNegInf) <= kMove - up()));
                     if (lane == 0)
                         loc->vote[sb][warp] = v;
                     // the maxima are the CTA's: any warp's vote moves them
@@ -1366,7 +1385,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (cc >= chunks)
                             break;
                         const int c = cc * 32 + lane;
-                        float M = fmaxf(fmaxf(scratch[c], scratch[64 + c]), fmaxf(scratch[128 + c], scratch[192 + c]));
+                        float M = fmaxf(fmaxf(scratch[c], scratch[64 + c]), fmaxf(scratch[128 + c], scratch[192 + c])) + up();
                         if (lead)
                             m_own[cc] = kNegInf;
                         M = M > m_own[cc] + kMove ? M : m_own[cc];
@@ -1534,7 +1553,8 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int first_masked = (s.len - s.n) / kTreeKeys;
             const int mine = min(R, s.n * G - s.rt * R) - warp * 32;   // this warp's rows of the tile
             const bool warp_on = mine > 0, real = lane < mine;
-            float m_used = kNegInf, l = 0.f;
+            const float up = tree_headroom<BF16>(s.len, 8);
+            float m_used = kNegInf, l = 0.f;         // the row's reference (maximum + up), its weights' sum
             uint64_t vis = 0ull;                     // of the last masked tile
             bool was_masked = false;
             // after P V of tile t - 1 (or the last one): what the scan took out of its V
@@ -1617,7 +1637,7 @@ tree_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             mx[(c >> 1) & 7] = fmax3(mx[(c >> 1) & 7], __uint_as_float(raw[c]), __uint_as_float(raw[c + 1]));
                         mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
                     }
-                    mt *= se;
+                    mt = BF16 ? fmaf(mt, se, up) : mt * se;
                     resc = real && mt > m_used + 8.f;
                     const float m_new = resc ? mt : m_used;
                     alpha = resc ? ex2(m_used - m_new) : 1.f;
@@ -2049,7 +2069,8 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             qf[ks][3] = __ldg(qb + ks * 8 + 4);
         }
     }
-    float m_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f}, acc[DT][4];
+    const float up = tree_headroom<BF16>(s.len, 8);
+    float m_run[2] = {kNegInf, kNegInf}, l_run[2] = {0.f, 0.f}, acc[DT][4];   // (references: maximum + up)
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -2140,7 +2161,8 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // the running maximum moves when a block exceeds it by 2^8
+            // the reference moves when a block's maximum exceeds the last by 2^8
+            mx += up;
             const bool move = mx > m_run[h] + 8.f;
             const float mnew = move ? mx : m_run[h];
             alpha[h] = move ? ex2(m_run[h] - mnew) : 1.f;
