@@ -100,6 +100,12 @@ pkv_status pkv_device_flags(int device, unsigned int *flags, int clear);
 pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, void *stream);
 
 /*
+ * The same for the wait of the tree attention kernels, which is bounded by a
+ * fixed number of tries (about two seconds) instead of a time.
+ */
+pkv_status pkv_selftest_counted_wait(void *stream);
+
+/*
  * kv_cache_write -- store the current tokens' K/V into their cache cells
  * ([MH] 2.1, 3.3; cache shape [YK] 三).
  *

@@ -29,6 +29,7 @@ from .pagedkv import (  # noqa: F401
     paged_attention_prefill,
     paged_attention_tree,
     selftest_bounded_wait,
+    selftest_counted_wait,
     tree_workspace_bytes,
     version,
 )

@@ -423,6 +423,15 @@ pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, void *stream)
     return PKV_OK;
 }
 
+pkv_status pkv_selftest_counted_wait(void *stream)
+{
+    pkv::counted_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return cuda_fail(e, "counted_wait_selftest_kernel launch");
+    return PKV_OK;
+}
+
 pkv_status pkv_kv_cache_write(const void *key, const void *value, const int64_t *slot_mapping,
                               int64_t num_tokens, int num_kv_heads, int head_dim, void *key_cache,
                               void *value_cache, int64_t num_blocks, int block_size,

@@ -782,6 +782,20 @@ __global__ void bounded_wait_selftest_kernel(uint64_t limit_ns)
         raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
 }
 
+// The same through the wait that the tree attention kernels use, which counts
+// its tries.
+__global__ void counted_wait_selftest_kernel()
+{
+    __shared__ __align__(8) uint64_t bar;
+    if (threadIdx.x == 0)
+        mbar_init(smem_addr(&bar), 1);
+    fence_mbar_init();
+    __syncwarp();
+    const bool got = mbar_wait_tries(smem_addr(&bar), 0u);
+    if (!__all_sync(0xffffffffu, got) && threadIdx.x == 0)
+        raise_flag(PKV_DEVFLAG_WAIT_TIMEOUT);
+}
+
 // ---------------------------------------------------------------------------
 // Log-sum-exp merge of split partitions
 // ---------------------------------------------------------------------------

@@ -65,6 +65,8 @@ def lib() -> ctypes.CDLL:
         L.pkv_copy_blocks.argtypes = [P, P, P, P, P, i32, i64, i64, i64, P]
         L.pkv_selftest_bounded_wait.restype = i32
         L.pkv_selftest_bounded_wait.argtypes = [i64, P]
+        L.pkv_selftest_counted_wait.restype = i32
+        L.pkv_selftest_counted_wait.argtypes = [P]
         L.pkv_kv_cache_write.restype = i32
         L.pkv_kv_cache_write.argtypes = [P, P, P, i64, i32, i32, P, P, i64, i32, i32, P]
         L.pkv_decode_plan.restype = i32
@@ -213,6 +215,12 @@ def selftest_bounded_wait(limit_ns: int, stream: Optional[torch.cuda.Stream] = N
     dev = torch.device("cuda", torch.cuda.current_device())
     _check(lib().pkv_selftest_bounded_wait(int(limit_ns), _stream_handle(stream, dev)),
            "pkv_selftest_bounded_wait")
+
+
+def selftest_counted_wait(stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Launch the counted-wait self-test kernel (see pkv_selftest_counted_wait)."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    _check(lib().pkv_selftest_counted_wait(_stream_handle(stream, dev)), "pkv_selftest_counted_wait")
 
 
 def hbm_read_probe(buf: torch.Tensor, sink: torch.Tensor, grid: int,

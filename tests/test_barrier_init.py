@@ -15,7 +15,7 @@ import pytest
 from paged_kv_cache_468_b200 import build
 
 USE = re.compile(r"\b(?:mbar_arrive\w*|mbar_wait\w*|mbar_try_wait|tma_load_\w+|bulk_load|tc_commit)\s*\(")
-WARP = {"compact_long_kernel", "bounded_wait_selftest_kernel"}   # kernels of one warp
+WARP = {"compact_long_kernel", "bounded_wait_selftest_kernel", "counted_wait_selftest_kernel"}   # kernels of one warp
 
 
 def _code(text):
