@@ -413,9 +413,19 @@ pkv_status pkv_draft_tree_mask(const int32_t *parents, int num_tokens, const int
  *   out = sum_j softmax_j(scale <q, K_j>) V_j   over the cells j of b with
  *   j < context_lens[b] - n_b, or bit j - (context_lens[b] - n_b) of i's row
  * with the softmax over exactly these cells; none of them gives a zero row.
- * Cells past context_lens[b] are never read.  Shapes as for the other calls
- * (group size 1..8, head_dim 64 / 128, block_size 16 / 32); max_query_len <=
- * PKV_TREE_MAX_NODES, else PKV_ERR_UNSUPPORTED.
+ * Cells past context_lens[b] are never read.
+ *
+ * The kernel and the workspace are chosen from the call's sizes alone, with
+ * max_blocks * block_size taken for the longest context: any wider table is
+ * right, but a tight one is faster (one that is far too wide costs short
+ * contexts up to 1.6 times the time).  The plan also decides whether the weights
+ * enter the product with V as two 16-bit parts (most calls of up to 16 query
+ * rows per kv head: about 16 bits in bf16, 22 in f16) or rounded to the caches'
+ * type, as in prefill.  Scores, sums and outputs are accumulated in 32 bits;
+ * bf16 values may be as large as the type holds.
+ *
+ * Shapes as for the other calls (group size 1..8, head_dim 64 / 128, block_size
+ * 16 / 32); max_query_len <= PKV_TREE_MAX_NODES, else PKV_ERR_UNSUPPORTED.
  */
 size_t pkv_tree_workspace_bytes(int batch, int max_query_len, int num_tokens, int num_heads,
                                 int num_kv_heads, int head_dim, int max_blocks, int block_size);

@@ -1932,7 +1932,7 @@ tree_merge_kernel(const TreeArgs a)
 //   S[rows x keys] = Q K^T      mma.sync m16n8k16, Q as A, K rows as B
 //   O[rows x D]   += P V        P straight from S's registers as A, V as B
 // P is split into a 16-bit high part and a 16-bit remainder, each multiplied
-// by V, so the weights keep about 16 bits more.  A CTA takes part_tokens keys
+// by V: the weights keep about 16 bits (bf16) or 22.  A CTA takes part_tokens keys
 // of a (sequence, kv head), a warp every other page of them.  An item of one
 // part is written out, of several as records that tree_rows_merge_kernel joins.
 // Bound by the cache's bytes: 256 x 512 .. 640 tokens, 8 kv heads of 128, 2
