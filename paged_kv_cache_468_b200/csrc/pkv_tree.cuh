@@ -402,8 +402,9 @@ __device__ __forceinline__ int tree_ctas(int total, int most)      // CTAs (or p
 // it, and weights that vanish now are below 2^-80 of the largest.  What it costs
 // are bits of sums of the smallest values, as 32-bit subnormals: over 1300 keys
 // the outputs are as exact as ever for values from 2^-118 (transposed: 2^-112)
-// to 2^128, and lose bits below (values of 2^-124: 0.6 %, transposed 20 %).  No
-// time.  f16 has neither such values nor the range for such weights.
+// to 2^128, and lose bits below (values of 2^-124: 0.6 %, transposed 20 %).
+// Times stay within 1 % (one user's 4000 tokens, few rows: 15.6 to 16.0 us).  f16
+// has neither such values nor the range for such weights.
 template <bool BF16>
 __device__ __forceinline__ float tree_headroom(int len, int move)
 {
